@@ -7,6 +7,7 @@ a GPU is missing, calls raise.
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import math
 import os
@@ -44,6 +45,7 @@ def _kv_kind(k, D: int, kv_dtype: str | None) -> int:
 EXPORTS = [
     "attn_prefill", "attn_decode_workspace_bytes", "attn_decode_num_splits", "attn_decode_splitkv",
     "attn_decode_splitkv_noalloc", "attn_decode_paged", "attn_prefill_varlen", "attn_decode_multi", "attn_decode_multi_workspace_bytes",
+    "attn_decode_tree_workspace_bytes", "attn_decode_tree", "attn_decode_tree_paged",
     "attn_merge_lse", "attn_stream_plan", "attn_stream_task", "attn_chunked_stream", "attn_status_string",
     "attn_last_cuda_error", "attn_device_status", "attn_set_wait_limit_ns", "attn_debug_wait_probe",
     "attn_debug_inject", "attn_debug_exp2",
@@ -156,6 +158,12 @@ def lib() -> ctypes.CDLL:
     L.attn_decode_multi_workspace_bytes.restype = sz
     L.attn_decode_multi.argtypes = [vp, vp, vp, i, vp, vp, vp, i, i, Dims, i, vp, vp, vp, sz, vp]
     L.attn_decode_multi.restype = i
+    L.attn_decode_tree_workspace_bytes.argtypes = [Dims, i, i]
+    L.attn_decode_tree_workspace_bytes.restype = sz
+    L.attn_decode_tree.argtypes = [vp, vp, vp, i, vp, vp, vp, vp, vp, i, i, Dims, vp, vp, vp, sz, vp]
+    L.attn_decode_tree.restype = i
+    L.attn_decode_tree_paged.argtypes = [vp, vp, vp, i, vp, vp, vp, i, i, i, vp, vp, vp, i, Dims, vp, vp, vp, sz, vp]
+    L.attn_decode_tree_paged.restype = i
     L.attn_merge_lse.argtypes = [vp, vp, i, ll, i, vp, i, vp, i, vp]
     L.attn_merge_lse.restype = i
     L.attn_stream_plan.argtypes = [Dims, ll, i, ll, sz, ctypes.POINTER(StreamPlan)]
@@ -208,6 +216,33 @@ def _need_cuda(*ts):
     for t in ts:
         if t is not None and not t.is_cuda:
             raise ValueError("device tensors expected (the library runs on the GPU only)")
+
+
+def _one_device(**ts):
+    """Every tensor of the call on one CUDA device, which is returned."""
+    _need_cuda(*ts.values())
+    devs = {t.device for t in ts.values() if t is not None}
+    if len(devs) != 1:
+        raise ValueError(f"tensors on one device expected, got {sorted(map(str, devs))}")
+    return devs.pop()
+
+
+@contextlib.contextmanager
+def _on(device, stream):
+    """Make `device`, and `stream` when one is given, torch's current ones while outputs and workspace are
+    allocated and the call is made: memory from another stream's pool could be handed out again
+    while the kernels still use it.  Yields the stream to pass to the library."""
+    with contextlib.ExitStack() as ctx:
+        if device.index != torch.cuda.current_device():
+            ctx.enter_context(torch.cuda.device(device))
+        if stream is not None:
+            if not isinstance(stream, torch.cuda.Stream):
+                h = int(stream)
+                stream = torch.cuda.ExternalStream(h, device=device) if h else torch.cuda.default_stream(device)
+            if stream.device != device:
+                raise ValueError(f"stream: expected one of {device}, got one of {stream.device}")
+            ctx.enter_context(torch.cuda.stream(stream))
+        yield _stream(stream)
 
 
 def _bshd_strides(name, t, dtypes, shape):
@@ -377,6 +412,71 @@ def attn_decode_paged(q, k_pool, v_pool, page_table, kv_lens, *, k_scale=None, v
                                  ws_bytes, _stream(stream))
     _check(st, "attn_decode_paged")
     return o, lse
+
+
+def attn_decode_tree_workspace_bytes(B, Hq, Hkv, D, Tmax, n_q, scale=1.0) -> int:
+    return int(lib().attn_decode_tree_workspace_bytes(_dims(B, Hq, Hkv, D, scale), int(Tmax), int(n_q)))
+
+
+def _decode_tree(name, q, k, v, kv_lens, tree_mask, q_lens, k_scale, v_scale, scale, o, lse, ws, want_lse, stream,
+                 kv_dtype, page_table):
+    device = _one_device(q=q, k=k, v=v, kv_lens=kv_lens, tree_mask=tree_mask, q_lens=q_lens, k_scale=k_scale,
+                         v_scale=v_scale, page_table=page_table, o=o, lse=lse, ws=ws)
+    if q.dim() != 4 or k.dim() != 4:
+        raise ValueError(f"q, k: expected 4 dimensions, got shapes {tuple(q.shape)} and {tuple(k.shape)}")
+    B, n_q, Hq, D = q.shape
+    Hkv = k.shape[2]
+    scale = 1.0 / math.sqrt(D) if scale is None else scale
+    kind = _kv_kind(k, D, kv_dtype)
+    _check_kv_rows(k, v, D, kind, k_scale, v_scale)
+    _check_decode_io(q, kv_lens, o, lse, ws, (B, n_q, Hq, D), None if page_table is not None else k.shape[0])
+    _expect("tree_mask", tree_mask, torch.int64, (B, n_q))
+    _expect("q_lens", q_lens, torch.int32, (B,))
+    if page_table is None:
+        Tmax = k.shape[1]
+    else:
+        if page_table.dim() != 2:
+            raise ValueError(f"page_table: expected int32 [B, max_pages], got shape {tuple(page_table.shape)}")
+        _expect("page_table", page_table, torch.int32, (B, page_table.shape[1]))
+        Tmax = page_table.shape[1] * k.shape[1]
+    dims = _dims(B, Hq, Hkv, D, scale)
+    with _on(device, stream) as st:
+        if o is None:
+            o = torch.empty((B, n_q, Hq, D), dtype=torch.bfloat16, device=device)
+        if lse is None and want_lse:
+            lse = torch.empty((B, n_q, Hq), dtype=torch.float32, device=device)
+        if ws is None:
+            need = int(lib().attn_decode_tree_workspace_bytes(dims, min(Tmax, 2**31 - 1), n_q))
+            ws = torch.empty(need, dtype=torch.uint8, device=device) if need else None
+        tail = (_ptr(q_lens), _ptr(tree_mask))
+        out = (_ptr(o), _ptr(lse), _ptr(ws), 0 if ws is None else ws.numel() * ws.element_size(), st)
+        head = (_ptr(q), _ptr(k), _ptr(v), kind, _ptr(k_scale), _ptr(v_scale))
+        if page_table is None:
+            rc = lib().attn_decode_tree(*head, _ptr(kv_lens), *tail, Tmax, n_q, dims, *out)
+        else:
+            rc = lib().attn_decode_tree_paged(*head, _ptr(page_table), page_table.shape[1], k.shape[1], k.shape[0],
+                                              _ptr(kv_lens), *tail, n_q, dims, *out)
+    _check(rc, name)
+    return o, lse
+
+
+def attn_decode_tree(q, k, v, kv_lens, tree_mask, *, q_lens=None, k_scale=None, v_scale=None,
+                     scale: float | None = None, o=None, lse=None, ws=None, want_lse: bool = True, stream=None,
+                     kv_dtype: str | None = None):
+    """q [B,n_q,Hq,D] bf16: up to 64 drafted tokens per sequence, already the cache's last q_lens[b] (int32
+    [B] on the device; None: n_q) tokens below kv_lens[b]; tree_mask int64 [B,n_q] on the device, bit j
+    of word i: draft i sees draft j; k/v as for attn_decode_splitkv (bf16 also with D = 64)
+    -> (o [B,n_q,Hq,D] bf16, lse [B,n_q,Hq] float32), rows past q_lens[b] 0 and -inf."""
+    return _decode_tree("attn_decode_tree", q, k, v, kv_lens, tree_mask, q_lens, k_scale, v_scale, scale, o, lse, ws,
+                        want_lse, stream, kv_dtype, None)
+
+
+def attn_decode_tree_paged(q, k_pool, v_pool, page_table, kv_lens, tree_mask, *, q_lens=None, k_scale=None,
+                           v_scale=None, scale: float | None = None, o=None, lse=None, ws=None,
+                           want_lse: bool = True, stream=None, kv_dtype: str | None = None):
+    """attn_decode_tree over a paged cache: pools, scale pools and page_table as for attn_decode_paged."""
+    return _decode_tree("attn_decode_tree_paged", q, k_pool, v_pool, kv_lens, tree_mask, q_lens, k_scale, v_scale,
+                        scale, o, lse, ws, want_lse, stream, kv_dtype, page_table)
 
 
 NOALLOC_SCRATCH_BYTES = 4 << 20

@@ -18,6 +18,7 @@
 #include "decode_int.cuh"
 #include "merge.cuh"
 #include "prefill.cuh"
+#include "tree.cuh"
 
 namespace attn {
 
@@ -75,6 +76,26 @@ static attn_status_t make_map_4d(CUtensorMap* map, const void* base, CUtensorMap
   cuuint32_t es[4] = {1, 1, 1, 1};
   CUresult r = fn(map, dt, 4, const_cast<void*>(base), gdim, gstride, bx, es, CU_TENSOR_MAP_INTERLEAVE_NONE, swz,
                   CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  if (r != CUDA_SUCCESS) {
+    t_last_cuda_error = (int)r;
+    return ATTN_ERR_CUDA;
+  }
+  return ATTN_OK;
+}
+
+// The queries of tree decode, [B, n_q, Hkv, G, D], as a 5-D map over (D, G, token, Hkv, B): a box holds the
+// G heads of one KV head for tps consecutive tokens (64 columns of them, 128-byte swizzle).
+static attn_status_t make_map_tree_q(CUtensorMap* map, const void* q, const attn_dims_t& d, int n_q, int tps) {
+  EncodeTiledFn fn = encode_fn();
+  if (!fn) return cuda_fail(cudaErrorNotSupported);
+  const cuuint64_t D = d.D, G = d.Hq / d.Hkv, Hq = d.Hq;
+  cuuint64_t gdim[5] = {D, G, (cuuint64_t)n_q, (cuuint64_t)d.Hkv, (cuuint64_t)d.B};
+  cuuint64_t gstride[4] = {D * 2, Hq * D * 2, G * D * 2, (cuuint64_t)n_q * Hq * D * 2};
+  cuuint32_t bx[5] = {64, (cuuint32_t)G, (cuuint32_t)tps, 1, 1};
+  cuuint32_t es[5] = {1, 1, 1, 1, 1};
+  CUresult r = fn(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 5, const_cast<void*>(q), gdim, gstride, bx, es,
+                  CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                  CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
   if (r != CUDA_SUCCESS) {
     t_last_cuda_error = (int)r;
     return ATTN_ERR_CUDA;
@@ -401,6 +422,133 @@ static attn_status_t launch_decode_kind(attn_dtype_t kv, const void* q, const vo
   }
 }
 
+// ---------------------------------------------------------------- tree decode
+
+// Row slots and ranges of a tree decode (tree.cuh): tps tokens per 128-row slot, two slots of rows per CTA
+// when one does not hold all n_q tokens, n_rb row blocks, n_groups ranges of key tiles.
+struct TreePlan {
+  int tps, pair, n_rb, n_groups, rows;
+};
+
+static TreePlan tree_plan(const attn_dims_t& d, int Tmax, int n_q) {
+  TreePlan t;
+  t.tps = std::min(128 / (d.Hq / d.Hkv), 64);
+  t.pair = n_q > t.tps;
+  const int slots = t.pair ? 2 : 1;
+  t.n_rb = (n_q + t.tps * slots - 1) / (t.tps * slots);
+  t.rows = 128 * slots;
+  int sms = 148, dev = 0;
+  if (cudaGetDevice(&dev) == cudaSuccess) cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
+  const long long tiles = (long long)d.B * d.Hkv * (((long long)Tmax + 127) / 128);
+  t.n_groups = (int)std::max(1LL, std::min<long long>(std::max(sms, 1) / t.n_rb, tiles));
+  return t;
+}
+
+static size_t tree_ws_bytes(const attn_dims_t& d, int Tmax, int n_q) {
+  if (Tmax <= 0 || d.B == 0) return 0;
+  const TreePlan t = tree_plan(d, Tmax, n_q);
+  return (size_t)t.n_groups * t.n_rb * 2 * t.rows * (d.D + 1) * sizeof(float);
+}
+
+template <int KIND, int D, bool PAIR>
+static attn_status_t launch_tree_inst(const CUtensorMap& mq, const CUtensorMap& mk, const CUtensorMap& mv,
+                                      const TreeParams& p, cudaStream_t stream) {
+  using C = TreeCfg<KIND, D, PAIR>;
+  static std::atomic<uint64_t> smem_done{0};
+  static std::atomic<int> regs_state{0};
+  attn_status_t st = ensure_smem(decode_tree_sm100<KIND, D, PAIR>, C::SMEM_BYTES, smem_done);
+  if (st != ATTN_OK) return st;
+  st = check_register_split(decode_tree_sm100<KIND, D, PAIR>, C::THREADS, C::REGS_TOTAL, regs_state);
+  if (st != ATTN_OK) return st;
+  decode_tree_sm100<KIND, D, PAIR><<<p.n_groups * p.n_rb, C::THREADS, C::SMEM_BYTES, stream>>>(mq, mk, mv, p);
+  ATTN_CUDA(cudaGetLastError());
+  return ATTN_OK;
+}
+
+template <int KIND, int D>
+static attn_status_t launch_tree(const void* q, const void* k, const void* v, const DecodePaging& pg,
+                                 const attn_dims_t& d, const TreePlan& t, TreeParams& p, cudaStream_t stream) {
+  attn_status_t st;
+  if (p.Tmax > 0) {
+    CUtensorMap mq, mk, mv;
+    constexpr bool CODED = KIND != TREE_BF16;
+    const uint64_t row = KIND == TREE_INT4 ? D / 2 : D;
+    const uint64_t dk[4] = {row, (uint64_t)d.Hkv, (uint64_t)pg.page_size, (uint64_t)pg.num_pages};
+    const uint32_t box[4] = {CODED ? (uint32_t)row : 64u, 1, 128, 1};
+    const CUtensorMapDataType dt = CODED ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16;
+    // Codes land unswizzled: their readers are the converter warps, not the MMA.
+    const CUtensorMapSwizzle swz = CODED ? CU_TENSOR_MAP_SWIZZLE_NONE : CU_TENSOR_MAP_SWIZZLE_128B;
+    if ((st = make_map_tree_q(&mq, q, d, p.n_q, t.tps)) != ATTN_OK) return st;
+    if ((st = make_map_4d(&mk, k, dt, CODED ? 1 : 2, dk, box, swz)) != ATTN_OK) return st;
+    if ((st = make_map_4d(&mv, v, dt, CODED ? 1 : 2, dk, box, swz)) != ATTN_OK) return st;
+    st = t.pair ? launch_tree_inst<KIND, D, true>(mq, mk, mv, p, stream)
+                : launch_tree_inst<KIND, D, false>(mq, mk, mv, p, stream);
+    if (st != ATTN_OK) return st;
+  }
+  const long long rows = (long long)d.B * p.n_q * d.Hq;
+  tree_join_kernel<D><<<(unsigned)((rows + 7) / 8), 256, 0, stream>>>(p, t.rows, t.pair ? 2 : 1);
+  ATTN_CUDA(cudaGetLastError());
+  return ATTN_OK;
+}
+
+// Checks and launch shared by the contiguous (pg.table null) and the paged entry point.
+static attn_status_t tree_call(const void* q, const void* k, const void* v, attn_dtype_t kv, const float* ks,
+                               const float* vs, const DecodePaging& pg, const int* kv_lens, const int* q_lens,
+                               const long long* mask, int Tmax, int n_q, const attn_dims_t& d, void* o, float* lse,
+                               void* ws, size_t ws_bytes, cudaStream_t stream) {
+  if (!q || !o || !kv_lens || !mask || (Tmax > 0 && (!k || !v))) return ATTN_ERR_INVALID_ARG;
+  const bool quant = kv != ATTN_BF16;  // codes + per-token scales
+  if (quant != (ks != nullptr) || quant != (vs != nullptr)) return ATTN_ERR_INVALID_ARG;
+  if (!aligned16(q) || !aligned16(o) || !aligned4(kv_lens) || (q_lens && !aligned4(q_lens)) ||
+      (reinterpret_cast<uintptr_t>(mask) & 7u) || (lse && !aligned4(lse)))
+    return ATTN_ERR_INVALID_ARG;
+  if (Tmax > 0 && (!aligned16(k) || !aligned16(v))) return ATTN_ERR_INVALID_ARG;
+  if (quant && (!aligned4(ks) || !aligned4(vs))) return ATTN_ERR_INVALID_ARG;
+  const int G = d.Hq / d.Hkv;
+  if (n_q > 64 || G > 128 || (d.D != 128 && (quant || d.D != 64))) return ATTN_ERR_UNSUPPORTED;
+  // Tiles, and rows of the join in blocks of 8, are int-indexed.
+  if (Tmax > 0x7fffff00 || (long long)d.B * d.Hkv > 0x7fffffffLL ||
+      (long long)d.B * d.Hkv * (((long long)Tmax + 127) / 128) > 0x7fffffffLL ||
+      (long long)d.B * d.Hq * n_q > 0x7fffffffLL)
+    return ATTN_ERR_UNSUPPORTED;
+  const size_t need = tree_ws_bytes(d, Tmax, n_q);
+  if (need > 0 && (!ws || ws_bytes < need || !aligned16(ws))) return ATTN_ERR_INVALID_ARG;
+  const TreePlan t = tree_plan(d, Tmax, n_q);
+  TreeParams p{};
+  p.B = d.B;
+  p.Hq = d.Hq;
+  p.Hkv = d.Hkv;
+  p.G = G;
+  p.Tmax = Tmax;
+  p.n_q = n_q;
+  p.tps = t.tps;
+  p.n_rb = t.n_rb;
+  p.n_groups = t.n_groups;
+  p.scale_log2 = d.scale * kLog2e;
+  p.kv_lens = kv_lens;
+  p.q_lens = q_lens;
+  p.mask = mask;
+  p.v = v;
+  p.k_scale = ks;
+  p.v_scale = vs;
+  p.page_table = pg.table;
+  p.max_pages = pg.max_pages;
+  p.page_size = std::max(pg.page_size, 1);
+  p.num_pages = pg.num_pages;
+  p.part_o = reinterpret_cast<float*>(ws);
+  p.part_lse = p.part_o + (size_t)t.n_groups * t.n_rb * 2 * t.rows * d.D;
+  p.o = reinterpret_cast<__nv_bfloat16*>(o);
+  p.lse = lse;
+  switch (kv) {
+    case ATTN_FP8_E4M3: return launch_tree<TREE_FP8, 128>(q, k, v, pg, d, t, p, stream);
+    case ATTN_INT8: return launch_tree<TREE_INT8, 128>(q, k, v, pg, d, t, p, stream);
+    case ATTN_INT4: return launch_tree<TREE_INT4, 128>(q, k, v, pg, d, t, p, stream);
+    default: break;
+  }
+  if (d.D == 64) return launch_tree<TREE_BF16, 64>(q, k, v, pg, d, t, p, stream);
+  return launch_tree<TREE_BF16, 128>(q, k, v, pg, d, t, p, stream);
+}
+
 // ---------------------------------------------------------------- diagnostics
 
 __global__ void exp2_probe_kernel(const float* x, float* y, long long n, int mode) {
@@ -679,6 +827,37 @@ attn_status_t attn_decode_multi(const void* q, const void* k, const void* v, att
   return launch_decode<KV_BF16>(q, k, v, nullptr, nullptr, kv_lens, Tmax, dims, P, per, o, lse, ws, st, pg, n_q);
 }
 
+size_t attn_decode_tree_workspace_bytes(attn_dims_t dims, int Tmax, int n_q) {
+  if (!dims_ok(dims) || dims.Hq / dims.Hkv > 128 || Tmax < 0 || n_q < 1 || n_q > 64) return 0;
+  return tree_ws_bytes(dims, Tmax, n_q);
+}
+
+attn_status_t attn_decode_tree(const void* q, const void* k, const void* v, attn_dtype_t kv_dtype,
+                               const float* k_scale, const float* v_scale, const int* kv_lens, const int* q_lens,
+                               const long long* tree_mask, int Tmax, int n_q, attn_dims_t dims, void* o, float* lse,
+                               void* ws, size_t ws_bytes, void* stream) {
+  if (!dims_ok(dims) || Tmax < 0 || n_q < 0 || !kv_dtype_ok(kv_dtype)) return ATTN_ERR_INVALID_ARG;
+  if (dims.B == 0 || n_q == 0) return ATTN_OK;
+  const DecodePaging pg{nullptr, 1, Tmax, dims.B};
+  return tree_call(q, k, v, kv_dtype, k_scale, v_scale, pg, kv_lens, q_lens, tree_mask, Tmax, n_q, dims, o, lse, ws,
+                   ws_bytes, reinterpret_cast<cudaStream_t>(stream));
+}
+
+attn_status_t attn_decode_tree_paged(const void* q, const void* k_pool, const void* v_pool, attn_dtype_t kv_dtype,
+                                     const float* k_scale_pool, const float* v_scale_pool, const int* page_table,
+                                     int max_pages, int page_size, int num_pages, const int* kv_lens,
+                                     const int* q_lens, const long long* tree_mask, int n_q, attn_dims_t dims, void* o,
+                                     float* lse, void* ws, size_t ws_bytes, void* stream) {
+  if (!dims_ok(dims) || n_q < 0 || !kv_dtype_ok(kv_dtype)) return ATTN_ERR_INVALID_ARG;
+  if (max_pages < 1 || page_size < 128 || page_size % 128 != 0 || num_pages < 1) return ATTN_ERR_INVALID_ARG;
+  if ((long long)max_pages * page_size > 0x7fffff00LL) return ATTN_ERR_UNSUPPORTED;
+  if (dims.B == 0 || n_q == 0) return ATTN_OK;
+  if (!page_table || !aligned4(page_table)) return ATTN_ERR_INVALID_ARG;
+  const DecodePaging pg{page_table, max_pages, page_size, num_pages};
+  return tree_call(q, k_pool, v_pool, kv_dtype, k_scale_pool, v_scale_pool, pg, kv_lens, q_lens, tree_mask,
+                   max_pages * page_size, n_q, dims, o, lse, ws, ws_bytes, reinterpret_cast<cudaStream_t>(stream));
+}
+
 // Split-KV decode without allocation: the split partials live in this static device array
 // (ATTN_NOALLOC_SCRATCH_BYTES per device, held until the process exits).  Host code must not pass
 // the array's name to a kernel — on the host it is only a stand-in — so its device address is
@@ -773,17 +952,20 @@ attn_status_t attn_merge_lse(const float* o_parts, const float* lse_parts, int P
 }
 
 attn_status_t attn_device_status(int reset, int* site) {
-  uint32_t v = 0;
+  uint32_t v = 0, a = 0;
   ATTN_CUDA(cudaDeviceSynchronize());
   ATTN_CUDA(cudaMemcpyFromSymbol(&v, g_dev_status, sizeof(v)));
+  ATTN_CUDA(cudaMemcpyFromSymbol(&a, g_arg_status, sizeof(a)));
   if (reset) {
     const uint32_t z = 0;
     ATTN_CUDA(cudaMemcpyToSymbol(g_dev_status, &z, sizeof(z)));
+    ATTN_CUDA(cudaMemcpyToSymbol(g_arg_status, &z, sizeof(z)));
   }
+  if (v == 0) v = a;
   if (site) *site = (int)(v & 0xFFFFu);
   if (v == 0) return ATTN_OK;
   if ((v >> 16) == ATTN_DEV_TIMEOUT) return ATTN_ERR_TIMEOUT;
-  if ((v >> 16) == ATTN_DEV_BAD_PAGE) return ATTN_ERR_INVALID_ARG;
+  if ((v >> 16) == ATTN_DEV_BAD_PAGE || (v >> 16) == ATTN_DEV_BAD_INDEX) return ATTN_ERR_INVALID_ARG;
   return ATTN_ERR_CUDA;
 }
 

@@ -1,0 +1,1058 @@
+// Attention of a tree of drafted tokens over a KV cache, on tcgen05.
+//
+// Several drafted tokens of a sequence, arranged as a tree, are verified in one pass over its cache
+// (ONNX Runtime packed-QSA analysis, "Code analysis" 2: multi-token verification).  The cache already
+// holds the drafts as its last tokens: with base = kv_len - q_len, token i sees slot t when t < base,
+// or when t < kv_len and bit (t - base) of its 64-bit mask is set:
+//     o_i = sum_t softmax_t(scale * q_i . k_t) v_t     over the slots t that token i sees.
+//
+// Rows.  The G query heads of a KV head share its keys, so row r = (i - i0) * G + g of a 128-row "slot"
+// is token i, head g of the group; a slot holds tps = floor(128 / G) tokens.  Q lands in that order
+// straight from [B, n_q, Hq, D] through a 5-D TMA box (64, G, tps, 1, 1).
+//   PAIR  (n_q > tps): the CTA's two slots are two row slots; every staged K/V tile feeds 256 rows.
+//         More than 256 rows are n_rb row blocks, run by neighbouring CTAs over the same tiles at
+//         the same time, so the cache crosses HBM once and the other blocks hit L2.
+//   !PAIR (n_q <= tps): the two slots hold the same rows and take alternate key tiles; their softmax
+//         states are joined in the epilogue.  One slot alone would leave the softmax of a tile
+//         and its two MMAs in series (~2300 cycles a tile against ~1450 of HBM time at 8 bits).
+//
+// Work.  The (sequence, KV head, 128-key tile) triples in that order are one line of W tiles, cut into
+// equal contiguous ranges, one per CTA (one per n_rb neighbouring CTAs): ragged lengths leave no CTA
+// with less to read, whatever Tmax is.  A range covers pieces of items (sequence, KV head); a piece
+// that is a whole item is finished here, another leaves a normalised partial in the workspace and
+// tree_join merges an item's partials in tile order (no atomics: results repeat bit for bit).
+//
+// Pipeline, as the prefill's: S = Q K^T in TMEM, one thread per row for the softmax, P (bf16) over S,
+// O += P V; unit ring of MMA-ready K and V tiles in consumption order.  Coded caches (E4M3, INT8, INT4)
+// land raw in a ring of their own and a fourth warpgroup widens them to bf16, which is exact for
+// every code; the K scale multiplies the fp32 score and the V scale the fp32 weight before its one
+// rounding to bf16, so no scale is rounded.
+//
+// Masked places.  Slots past kv_len and drafts no token sees are never used.  A draft that some tokens
+// see may hold anything too: its non-finite V elements enter the MMA as zeros (0 * NaN would reach
+// the rows that do not see it) and the epilogue adds them back to the rows that do.
+#pragma once
+
+#include "ptx.cuh"
+
+namespace attn {
+
+struct TreeParams {
+  int B, Hq, Hkv, G, Tmax, n_q;
+  int tps;       // tokens per 128-row slot
+  int n_rb;      // row blocks (CTAs that share a range of tiles)
+  int n_groups;  // ranges (grid = n_groups * n_rb)
+  float scale_log2;
+  const int* kv_lens;       // [B]
+  const int* q_lens;        // [B] or null (n_q)
+  const long long* mask;    // [B, n_q]
+  const void* v;            // the V cache again, for the epilogue's non-finite drafts
+  const float* k_scale;     // coded caches: [pages, page_size, Hkv]
+  const float* v_scale;
+  const int* page_table;    // [B, max_pages] or null (one page of Tmax tokens per sequence)
+  int max_pages, page_size, num_pages;
+  float* part_o;            // [n_groups * n_rb * 2, rows, D] normalised partials
+  float* part_lse;          // [n_groups * n_rb * 2, rows] their log2-domain log-sum-exp
+  __nv_bfloat16* o;         // [B, n_q, Hq, D]
+  float* lse;               // [B, n_q, Hq] or null
+};
+
+enum TreeKv { TREE_BF16 = 0, TREE_FP8 = 1, TREE_INT8 = 2, TREE_INT4 = 3 };
+
+__device__ __forceinline__ int tree_len(const TreeParams& p, int b) {
+  const int len = __ldg(p.kv_lens + b);
+  return len < 0 ? 0 : (len > p.Tmax ? p.Tmax : len);
+}
+__device__ __forceinline__ int tree_qlen(const TreeParams& p, int b) {
+  if (!p.q_lens) return p.n_q;
+  const int n = __ldg(p.q_lens + b);
+  return n < 0 ? 0 : (n > p.n_q ? p.n_q : n);
+}
+// Key tiles of one KV head of sequence b (none when it drafts nothing).
+__device__ __forceinline__ int tree_tiles(const TreeParams& p, int b) {
+  return tree_qlen(p, b) > 0 ? (tree_len(p, b) + 127) >> 7 : 0;
+}
+
+// Pool page of token tok of sequence b, -1 (never dereferenced: TMA fills zeros, scales read as 0) for a
+// table entry outside the pool, which is reported.
+__device__ __forceinline__ int tree_page(const TreeParams& p, int b, int tok) {
+  if (!p.page_table) return b;
+  const int pg = __ldg(p.page_table + (long long)b * p.max_pages + tok / p.page_size);
+  if (pg >= 0 && pg < p.num_pages) return pg;
+  record_arg_error(ATTN_DEV_BAD_PAGE, SITE_TR_PAGE);
+  return -1;
+}
+__device__ __forceinline__ int tree_page_off(const TreeParams& p, int tok) {
+  return p.page_table ? tok % p.page_size : tok;
+}
+
+// Where the range of group g starts: floor(g * W / ng).
+__device__ __forceinline__ int tree_range(int g, int W, int ng) { return (int)((long long)g * W / ng); }
+
+struct TreePiece {
+  int b, kvh, t0, n;  // tiles t0 .. t0 + n - 1 of (sequence, KV head)
+  int len, qn;        // the sequence's cache length and drafted tokens
+  int which;          // 0: the first piece of this CTA's range, 1: a later one (names its partial)
+  bool whole;         // every tile of the item
+};
+
+// The pieces of a CTA's range, in order; every role walks its own copy.
+struct TreeWalk {
+  int left, b, kvh, tile, idx;
+  int len, qn, tiles;
+  __device__ __forceinline__ void load(const TreeParams& p) {
+    len = tree_len(p, b);
+    qn = tree_qlen(p, b);
+    tiles = qn > 0 ? (len + 127) >> 7 : 0;
+  }
+  // s: {tiles of the range, first sequence, tile offset within that sequence's Hkv * tiles}
+  __device__ __forceinline__ void init(const TreeParams& p, const int* s) {
+    left = s[0];
+    b = s[1];
+    idx = 0;
+    kvh = tile = 0;
+    if (left > 0) {
+      load(p);
+      kvh = s[2] / tiles;
+      tile = s[2] - kvh * tiles;
+    }
+  }
+  __device__ __forceinline__ bool next(const TreeParams& p, TreePiece& out) {
+    if (left <= 0) return false;
+    while (kvh == p.Hkv || tiles == 0) {  // left > 0: a later sequence has tiles
+      ++b;
+      kvh = 0;
+      load(p);
+    }
+    const int n = min(tiles - tile, left);
+    out.b = b;
+    out.kvh = kvh;
+    out.t0 = tile;
+    out.n = n;
+    out.len = len;
+    out.qn = qn;
+    out.which = idx > 0;
+    out.whole = n == tiles;
+    ++idx;
+    left -= n;
+    tile += n;
+    if (tile == tiles) {
+      tile = 0;
+      ++kvh;
+    }
+    return true;
+  }
+};
+
+// One warp: total tiles, this group's range, and the sequence it starts in -> s[0..2].
+__device__ __forceinline__ void tree_find_range(const TreeParams& p, int g, int lane, int* s) {
+  int total = 0;
+  for (int b = lane; b < p.B; b += 32) total += tree_tiles(p, b);
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) total += __shfl_xor_sync(0xffffffffu, total, o);
+  const int W = total * p.Hkv;
+  const int ng = min(p.n_groups, W);
+  int left = 0, start = 0;
+  if (g < ng) {
+    start = tree_range(g, W, ng);
+    left = tree_range(g + 1, W, ng) - start;
+  }
+  int b0 = 0, off = 0, before = 0;
+  if (left > 0) {
+    for (int c = 0; c < p.B; c += 32) {
+      const int b = c + lane;
+      const int n = (b < p.B ? tree_tiles(p, b) : 0) * p.Hkv;
+      int incl = n;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const int y = __shfl_up_sync(0xffffffffu, incl, o);
+        if (lane >= o) incl += y;
+      }
+      const uint32_t hit = __ballot_sync(0xffffffffu, before + incl > start);
+      if (hit) {
+        const int src = __ffs(hit) - 1;
+        b0 = c + src;
+        off = start - (before + __shfl_sync(0xffffffffu, incl - n, src));
+        break;
+      }
+      before += __shfl_sync(0xffffffffu, incl, 31);
+    }
+  }
+  if (lane == 0) {
+    s[0] = left;
+    s[1] = b0;
+    s[2] = off;
+  }
+}
+
+template <int KIND, int D, bool PAIR>
+struct TreeCfg {
+  static constexpr bool CODED = KIND != TREE_BF16;
+  static constexpr int BOX_BYTES = 128 * 128;  // 128 rows x 64 bf16
+  static constexpr int NBOX = D / 64;
+  static constexpr int TILE_BYTES = NBOX * BOX_BYTES;
+  static constexpr int NQ = PAIR ? 2 : 1;  // Q slots in shared memory
+  // MMA-ready units in flight, raw units in flight (coded caches), scale tiles in flight.
+  static constexpr int NU = D == 64 ? 6 : (CODED ? (PAIR ? 3 : 4) : 5);
+  static constexpr int RAW_BYTES = 128 * (KIND == TREE_INT4 ? D / 2 : D);
+  static constexpr int NR = CODED ? (KIND == TREE_INT4 ? 6 : 3) : 0;
+  static constexpr int NS = CODED ? 4 : 0;
+  static constexpr int OFF_Q = 0;
+  static constexpr int OFF_U = OFF_Q + NQ * TILE_BYTES;
+  static constexpr int OFF_RAW = OFF_U + NU * TILE_BYTES;
+  static constexpr int OFF_SC = OFF_RAW + NR * RAW_BYTES;      // [NS][2][128] floats
+  static constexpr int OFF_ML = OFF_SC + NS * 1024;            // [2 slots][128] (max, sum) of the halves
+  static constexpr int OFF_BAR = OFF_ML + (PAIR ? 0 : 2048);
+  static constexpr int N_BARS = 2 + 2 * NU + 2 * NR + 2 * NS + 2 + 2 + 2 + 2 + 1;
+  static constexpr int SMEM_BYTES = OFF_BAR + N_BARS * 8 + 64 + 1024;  // + walk start, flags, alignment slack
+  static constexpr int THREADS = CODED ? 512 : 384;
+  // Register split: control warpgroup, converter warpgroup, two softmax warpgroups; the sum never
+  // exceeds what the launch holds (checked on the host before the first launch).
+  static constexpr int REGS_CTRL = CODED ? 64 : 72;
+  static constexpr int REGS_CONV = 80;
+  static constexpr int REGS_SOFTMAX = CODED ? 184 : 216;
+  static constexpr int REGS_TOTAL = REGS_CTRL * 128 + (CODED ? REGS_CONV * 128 : 0) + REGS_SOFTMAX * 256;
+  static constexpr uint32_t TMEM_COLS = 512;
+  static constexpr float RESCALE_THRESHOLD = 8.0f;
+  static constexpr int ROWS = PAIR ? 256 : 128;  // rows of a partial
+};
+
+// Unit order within a piece of n tiles (units K(0..n-1), V(0..n-1); 2n in all).
+//   PAIR: K0 V0 K1 V1 ...            !PAIR: K0 K1 V0 K2 V1 K3 V2 ...
+template <bool PAIR>
+__device__ __forceinline__ int tree_v_unit(int j, int n) {
+  return PAIR ? 2 * j + 1 : min(j + 2, n) + j;
+}
+
+// Two codes (16 bits, first in the low byte) -> two bf16, exact.
+__device__ __forceinline__ uint32_t e4m3x2_to_bf16x2(uint16_t c) {
+  const uint32_t h = e4m3x2_to_f16x2(c);
+  const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&h));
+  return pack_bf16x2(f.x, f.y);
+}
+__device__ __forceinline__ uint32_t bf16x2_sub(uint32_t a, uint32_t b) {
+  uint32_t r;
+  asm("sub.rn.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+  return r;
+}
+// INT8: the code c in byte form is 7 value bits u and a sign bit s, c = u - 128 s.  0x4300 | u is the bf16
+// 128 + u (one unit in the last place is 1 there) and 0x4300 | (s << 7) is 128 or 256, so their
+// difference is c exactly.
+__device__ __forceinline__ uint32_t int8x2_to_bf16x2(uint32_t w, uint32_t sel) {
+  uint32_t v;
+  asm("prmt.b32 %0, %1, 0, %2;" : "=r"(v) : "r"(w), "r"(sel));  // codes in the low bytes of two 16-bit lanes
+  return bf16x2_sub((v & 0x007f007fu) | 0x43004300u, (v & 0x00800080u) | 0x43004300u);
+}
+
+// 16 raw codes -> 32 bytes of bf16 (two 16-byte chunks).
+template <int KIND>
+__device__ __forceinline__ void tree_widen(const uint32_t (&w)[4], uint4& lo, uint4& hi) {
+  uint32_t r[8];
+  if constexpr (KIND == TREE_FP8) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      r[2 * i] = e4m3x2_to_bf16x2((uint16_t)(w[i] & 0xffffu));
+      r[2 * i + 1] = e4m3x2_to_bf16x2((uint16_t)(w[i] >> 16));
+    }
+  } else if constexpr (KIND == TREE_INT8) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      r[2 * i] = int8x2_to_bf16x2(w[i], 0x4140);
+      r[2 * i + 1] = int8x2_to_bf16x2(w[i], 0x4342);
+    }
+  } else {
+    // INT4: nibble n of a word is element n.  (c ^ 8) in 0..15 is c + 8; 0x4300 | (c + 8) is 136 + c.
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      uint32_t e[4];  // e[k]: elements k (low lane) and k + 4 (high lane)
+#pragma unroll
+      for (int k = 0; k < 4; ++k)
+        e[k] = bf16x2_sub(((w[i] >> (4 * k)) & 0x000f000fu) ^ 0x43084308u, 0x43084308u);
+      r[4 * i + 0] = __byte_perm(e[0], e[1], 0x5410);
+      r[4 * i + 1] = __byte_perm(e[2], e[3], 0x5410);
+      r[4 * i + 2] = __byte_perm(e[0], e[1], 0x7632);
+      r[4 * i + 3] = __byte_perm(e[2], e[3], 0x7632);
+    }
+  }
+  lo = make_uint4(r[0], r[1], r[2], r[3]);
+  hi = make_uint4(r[4], r[5], r[6], r[7]);
+}
+
+// Non-finite bf16 elements of a packed pair set to zero; true if there was one.
+__device__ __forceinline__ bool bf16x2_drop_nonfinite(uint32_t& w) {
+  bool bad = false;
+  if ((w & 0x7f80u) == 0x7f80u) {
+    w &= 0xffff0000u;
+    bad = true;
+  }
+  if ((w & 0x7f800000u) == 0x7f800000u) {
+    w &= 0x0000ffffu;
+    bad = true;
+  }
+  return bad;
+}
+
+// One V element of the cache as float (the epilogue's slow path).
+template <int KIND, int D>
+__device__ __forceinline__ float tree_v_value(const TreeParams& p, long long row, int d) {
+  if constexpr (KIND == TREE_BF16) {
+    return __bfloat162float(reinterpret_cast<const __nv_bfloat16*>(p.v)[row * D + d]);
+  } else {
+    float c;
+    if constexpr (KIND == TREE_INT8) {
+      c = (float)reinterpret_cast<const int8_t*>(p.v)[row * D + d];
+    } else if constexpr (KIND == TREE_INT4) {
+      const int x = reinterpret_cast<const uint8_t*>(p.v)[row * (D / 2) + (d >> 1)];
+      const int n = (d & 1) ? x >> 4 : x & 15;
+      c = (float)(n >= 8 ? n - 16 : n);
+    } else {
+      const uint32_t h = e4m3x2_to_f16x2(reinterpret_cast<const uint8_t*>(p.v)[row * D + d]);
+      c = __low2float(*reinterpret_cast<const __half2*>(&h));
+    }
+    return c * p.v_scale[row];
+  }
+}
+
+// Every draft that some token of sequence b sees, as a 64-bit set (warp-collective).
+__device__ __forceinline__ unsigned long long tree_seen_any(const TreeParams& p, int b, int qn, int lane) {
+  const long long* m = p.mask + (long long)b * p.n_q;
+  unsigned long long x = 0;
+  if (lane < qn) x |= (unsigned long long)__ldg(m + lane);
+  if (lane + 32 < qn) x |= (unsigned long long)__ldg(m + lane + 32);
+  const uint32_t lo = __reduce_or_sync(0xffffffffu, (uint32_t)x);
+  const uint32_t hi = __reduce_or_sync(0xffffffffu, (uint32_t)(x >> 32));
+  return ((unsigned long long)hi << 32) | lo;
+}
+
+__device__ __forceinline__ unsigned long long tree_low_bits(int n) {
+  return n >= 64 ? ~0ull : (1ull << n) - 1ull;
+}
+
+// Columns of the tile at kv0 that a row sees, 32 of them as a word: slots below base, and drafts in m.
+__device__ __forceinline__ uint32_t tree_seen_word(int w, int kv0, int base, unsigned long long m) {
+  const int pre = base - kv0 - 32 * w;  // leading columns of this word that are below base
+  uint32_t x = pre <= 0 ? 0u : (pre >= 32 ? ~0u : (1u << pre) - 1u);
+  const int q = -pre;  // the draft that column 0 of the word would be
+  if (q > -32 && q < 64) x |= q < 0 ? (uint32_t)(m << -q) : (uint32_t)(m >> q);
+  return x;
+}
+
+template <int KIND, int D, bool PAIR>
+__global__ void __launch_bounds__((TreeCfg<KIND, D, PAIR>::THREADS), 1)
+    decode_tree_sm100(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
+                      const __grid_constant__ CUtensorMap tmV, const TreeParams p) {
+  using C = TreeCfg<KIND, D, PAIR>;
+  constexpr bool CODED = C::CODED;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  uint64_t* bars = reinterpret_cast<uint64_t*>(smem + C::OFF_BAR);
+  // Phases: q_*, o_*, ml_* complete once per piece (qi); u_full / u_empty once per use of a unit (u);
+  // raw_* once per raw unit, sc_* once per tile, s_full / p_full once per tile of their slot.
+  uint64_t* q_full = bars;
+  uint64_t* q_empty = bars + 1;
+  uint64_t* u_full = bars + 2;
+  uint64_t* u_empty = u_full + C::NU;
+  uint64_t* raw_full = u_empty + C::NU;
+  uint64_t* raw_empty = raw_full + C::NR;
+  uint64_t* sc_full = raw_empty + C::NR;
+  uint64_t* sc_empty = sc_full + C::NS;
+  uint64_t* s_full = sc_empty + C::NS;  // [2]
+  uint64_t* p_full = s_full + 2;        // [2]
+  uint64_t* o_full = p_full + 2;
+  uint64_t* o_empty = o_full + 1;
+  uint64_t* ml_full = o_empty + 1;      // the halves' (max, sum) are in shared memory (8 warps)
+  uint64_t* ml_empty = ml_full + 1;     // ... and have been read
+  uint64_t* drain = ml_empty + 1;
+  uint32_t* tmem_holder = reinterpret_cast<uint32_t*>(drain + 1);
+  int* walk0 = reinterpret_cast<int*>(tmem_holder + 1);   // [3]
+  // odd_piece[i & 7] = i + 1 when piece i holds a non-finite draft V.  Whoever finds one runs at most a
+  // ring of units ahead of the epilogue that asks (NU <= 6, two units or more a piece): eight entries.
+  int* odd_piece = walk0 + 3;
+
+  const int warp = threadIdx.x >> 5;
+  const int lane = threadIdx.x & 31;
+  const int rb = (int)blockIdx.x % p.n_rb;
+
+  if (threadIdx.x == 0) {
+    mbar_init(q_full, 1);
+    mbar_init(q_empty, 1);
+    for (int i = 0; i < C::NU; ++i) {
+      mbar_init(&u_full[i], CODED ? 4 : 1);  // converter warps, or the producer's expect_tx
+      mbar_init(&u_empty[i], 1);
+    }
+    for (int i = 0; i < C::NR; ++i) {
+      mbar_init(&raw_full[i], 1);
+      mbar_init(&raw_empty[i], 4);
+    }
+    for (int i = 0; i < C::NS; ++i) {
+      mbar_init(&sc_full[i], 4);
+      mbar_init(&sc_empty[i], PAIR ? 8 : 4);
+    }
+    for (int s = 0; s < 2; ++s) {
+      mbar_init(&s_full[s], 1);
+      mbar_init(&p_full[s], 4);
+    }
+    mbar_init(o_full, 1);
+    mbar_init(o_empty, 8);
+    mbar_init(ml_full, 8);
+    mbar_init(ml_empty, 8);
+    mbar_init(drain, 1);
+    for (int i = 0; i < 8; ++i) odd_piece[i] = 0;
+    fence_barrier_init();
+  }
+  if (warp == 1) {
+    tmem_alloc(tmem_holder, C::TMEM_COLS);
+    tmem_relinquish();
+  }
+  if (warp == 2) tree_find_range(p, (int)blockIdx.x / p.n_rb, lane, walk0);
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *tmem_holder;
+
+  if (warp == 0) {
+    // ------------------------------------------------------------------ TMA producer
+    regs_dec<C::REGS_CTRL>();
+    if (lane == 0) {
+      tma_prefetch_desc(&tmQ);
+      tma_prefetch_desc(&tmK);
+      tma_prefetch_desc(&tmV);
+      // A tile is read by the n_rb CTAs of its group at about the same time and never again.
+      const uint64_t pol = l2_policy_evict_first();
+      const uint32_t q_box = (uint32_t)(p.tps * p.G) * 128u;
+      int u = 0, qi = 0;
+      bool ok = true, q_pending = false;
+      auto load = [&](const CUtensorMap* tm, const TreePiece& it, int j) -> bool {
+        const int tok = (it.t0 + j) * 128;
+        const int pg = tree_page(p, it.b, tok), off = tree_page_off(p, tok);
+        if constexpr (CODED) {
+          const int st = u % C::NR;
+          if (!mbar_wait<true>(&raw_empty[st], ((u / C::NR) & 1) ^ 1, SITE_TR_LOAD)) return false;
+          mbar_arrive_expect_tx(&raw_full[st], C::RAW_BYTES);
+          tma_load_4d_hint(smem + C::OFF_RAW + st * C::RAW_BYTES, tm, &raw_full[st], 0, it.kvh, off, pg, pol);
+        } else {
+          const int st = u % C::NU;
+          if (!mbar_wait<true>(&u_empty[st], ((u / C::NU) & 1) ^ 1, SITE_TR_LOAD)) return false;
+          mbar_arrive_expect_tx(&u_full[st], C::TILE_BYTES);
+          for (int bx = 0; bx < C::NBOX; ++bx)
+            tma_load_4d_hint(smem + C::OFF_U + st * C::TILE_BYTES + bx * C::BOX_BYTES, tm, &u_full[st], bx * 64,
+                             it.kvh, off, pg, pol);
+        }
+        ++u;
+        return true;
+      };
+      TreeWalk w;
+      TreePiece it;
+      w.init(p, walk0);
+      while (ok && w.next(p, it)) {
+        if (qi > 0 && !(ok = mbar_wait<true>(q_empty, (qi - 1) & 1, SITE_TR_LOAD))) break;
+        mbar_arrive_expect_tx(q_full, C::NQ * C::NBOX * q_box);
+        q_pending = true;
+        for (int s = 0; s < C::NQ; ++s)
+          for (int bx = 0; bx < C::NBOX; ++bx)
+            tma_load_5d(smem + C::OFF_Q + s * C::TILE_BYTES + bx * C::BOX_BYTES, &tmQ, q_full, bx * 64, 0,
+                        (rb * C::NQ + s) * p.tps, it.kvh, it.b);
+        if constexpr (PAIR) {
+          for (int j = 0; j < it.n && ok; ++j) ok = load(&tmK, it, j) && load(&tmV, it, j);
+        } else {
+          ok = load(&tmK, it, 0) && (it.n < 2 || load(&tmK, it, 1));
+          for (int j = 0; j < it.n && ok; ++j) ok = load(&tmV, it, j) && (j + 2 >= it.n || load(&tmK, it, j + 2));
+        }
+        if (!ok) break;
+        ++qi;
+        q_pending = false;
+      }
+      if (!ok) {
+        // Let every copy already issued land before the CTA's shared memory is released.
+        if (q_pending) mbar_wait_drain<true>(q_full, qi & 1, SITE_TR_DRAIN);
+        constexpr int N = CODED ? C::NR : C::NU;
+        uint64_t* full = CODED ? raw_full : u_full;
+        for (int t = (u > N ? u - N : 0); t < u; ++t) mbar_wait_drain<true>(&full[t % N], (t / N) & 1, SITE_TR_DRAIN);
+      }
+    }
+    __syncwarp();
+  } else if (warp == 1) {
+    // ------------------------------------------------------------------ MMA issuer
+    regs_dec<C::REGS_CTRL>();
+    {
+      constexpr uint32_t idesc_qk = make_idesc_f16(128, 128, false, false, true);
+      constexpr uint32_t idesc_pv = make_idesc_f16(128, D, false, true, true);
+      constexpr uint32_t HI = sdesc_sw128_hi(1024);
+      const uint32_t q_lo = sdesc_sw128_lo(smem_u32(smem + C::OFF_Q), 16);
+      const uint32_t k_lo = sdesc_sw128_lo(smem_u32(smem + C::OFF_U), 16);
+      const uint32_t v_lo = sdesc_sw128_lo(smem_u32(smem + C::OFF_U), C::BOX_BYTES);
+      auto issue_qk = [&](int s, int st) {
+        const uint32_t a0 = q_lo + (((PAIR ? s : 0) * C::TILE_BYTES) >> 4), b0 = k_lo + ((st * C::TILE_BYTES) >> 4);
+        const uint32_t d = tmem + s * 128;
+#pragma unroll
+        for (int kk = 0; kk < D / 16; ++kk) {
+          const uint32_t off = ((kk >> 2) * C::BOX_BYTES + (kk & 3) * 32) >> 4;
+          mma_ss_elect(d, sdesc_join(a0 + off, HI), sdesc_join(b0 + off, HI), idesc_qk, kk > 0);
+        }
+      };
+      auto issue_pv = [&](int s, int st, bool acc) {
+        const uint32_t b0 = v_lo + ((st * C::TILE_BYTES) >> 4);
+        const uint32_t d = tmem + 256 + s * D, a = tmem + s * 128;
+#pragma unroll
+        for (int kk = 0; kk < 128 / 16; ++kk)
+          mma_ts_elect(d, a + kk * 8, sdesc_join(b0 + ((kk * 16 * 128) >> 4), HI), idesc_pv,
+                       (acc || kk > 0) ? 1u : 0u);
+      };
+      int u = 0, qi = 0, c0 = 0, c1 = 0;  // units consumed, pieces, tiles of each slot
+      bool ok = true;
+      auto wait_unit = [&](int& st) -> bool {
+        st = u % C::NU;
+        const bool r = mbar_wait_warp<true>(&u_full[st], (u / C::NU) & 1, SITE_TR_MMA_U);
+        ++u;
+        return r;
+      };
+      TreeWalk w;
+      TreePiece it;
+      w.init(p, walk0);
+      while (ok && w.next(p, it)) {
+        const int n = it.n;
+        int st = 0;
+        if (!(ok = mbar_wait_warp<true>(q_full, qi & 1, SITE_TR_MMA_Q))) break;
+        if constexpr (PAIR) {
+          if (!(ok = wait_unit(st))) break;
+          tc_fence_after();
+          // S(0) of this piece overwrites S/P regions the previous piece's PVs read: those were
+          // issued earlier by this warp and the tensor pipe executes in order.
+          issue_qk(0, st);
+          mma_commit_elect(&s_full[0]);
+          issue_qk(1, st);
+          mma_commit_elect(&s_full[1]);
+          mma_commit_elect(&u_empty[st]);
+          if (n == 1) mma_commit_elect(q_empty);
+          for (int j = 0; j < n; ++j) {
+            const bool more = j + 1 < n;
+            int sv, sk = 0;
+            if (!(ok = wait_unit(sv))) break;
+            if (!(ok = mbar_wait_warp<true>(&p_full[0], c0 & 1, SITE_TR_MMA_P))) break;
+            if (j == 0 && qi > 0 && !(ok = mbar_wait_warp<true>(o_empty, (qi - 1) & 1, SITE_TR_MMA_P))) break;
+            tc_fence_after();
+            issue_pv(0, sv, j > 0);
+            if (more) {
+              if (!(ok = wait_unit(sk))) break;
+              tc_fence_after();
+              issue_qk(0, sk);
+              mma_commit_elect(&s_full[0]);
+            }
+            if (!(ok = mbar_wait_warp<true>(&p_full[1], c0 & 1, SITE_TR_MMA_P))) break;
+            tc_fence_after();
+            issue_pv(1, sv, j > 0);
+            mma_commit_elect(&u_empty[sv]);
+            if (more) {
+              issue_qk(1, sk);
+              mma_commit_elect(&s_full[1]);
+              mma_commit_elect(&u_empty[sk]);
+              if (j + 2 == n) mma_commit_elect(q_empty);
+            }
+            ++c0;
+          }
+        } else {
+          for (int s = 0; s < 2 && s < n; ++s) {
+            if (!(ok = wait_unit(st))) break;
+            tc_fence_after();
+            issue_qk(s, st);
+            mma_commit_elect(&s_full[s]);
+            mma_commit_elect(&u_empty[st]);
+          }
+          if (!ok) break;
+          if (n <= 2) mma_commit_elect(q_empty);
+          for (int j = 0; j < n; ++j) {
+            const int s = j & 1;
+            if (!(ok = wait_unit(st))) break;
+            if (!(ok = mbar_wait_warp<true>(&p_full[s], (s ? c1 : c0) & 1, SITE_TR_MMA_P))) break;
+            if (j == 0 && qi > 0 && !(ok = mbar_wait_warp<true>(o_empty, (qi - 1) & 1, SITE_TR_MMA_P))) break;
+            tc_fence_after();
+            issue_pv(s, st, j > 1);
+            mma_commit_elect(&u_empty[st]);
+            if (j + 2 < n) {
+              if (!(ok = wait_unit(st))) break;
+              tc_fence_after();
+              issue_qk(s, st);
+              mma_commit_elect(&s_full[s]);
+              mma_commit_elect(&u_empty[st]);
+              if (j + 3 == n) mma_commit_elect(q_empty);
+            }
+            if (s) ++c1;
+            else ++c0;
+          }
+        }
+        if (!ok) break;
+        mma_commit_elect(o_full);
+        ++qi;
+      }
+      // Drain: every MMA issued above completes before TMEM is released.
+      mma_commit_elect(drain);
+      mbar_wait_drain<true>(drain, 0, SITE_TR_DRAIN);
+    }
+    __syncwarp();
+  } else if (warp < 4) {
+    regs_dec<C::REGS_CTRL>();
+  } else if (CODED && warp >= 12) {
+    // ------------------------------------------------------------------ converters
+    if constexpr (CODED) {
+      regs_dec<C::REGS_CONV>();
+      const int cw = warp - 12, t = cw * 32 + lane;
+      // Lane l of a warp widens 16 codes: row pair 2 (l >> 3) + ((l >> 2) & 1) of eight rows, 16-code column c.  The
+      // two rows of a pair take columns 0-3 and 4-7, so the eight lanes of a phase read 128 distinct
+      // bytes and their two 16-byte results go to eight distinct chunks of the swizzled tile.
+      const int sub = lane & 7, hi_row = sub >> 2;
+      int u = 0, g = 0, qi = 0;
+      bool ok = true;
+      auto convert = [&](const TreePiece& it, int j, bool is_v) -> bool {
+        const int rs = u % C::NR, st = u % C::NU;
+        bool r = mbar_wait_warp<true>(&raw_full[rs], (u / C::NR) & 1, SITE_TR_CONV);
+        r = r && mbar_wait_warp<true>(&u_empty[st], ((u / C::NU) & 1) ^ 1, SITE_TR_CONV);
+        if (!r) return false;
+        const uint8_t* raw = smem + C::OFF_RAW + rs * C::RAW_BYTES;
+        uint8_t* dst = smem + C::OFF_U + st * C::TILE_BYTES;
+        const int kv0 = (it.t0 + j) * 128, base = it.len - it.qn;
+        const bool edge = is_v && kv0 + 128 > base;
+        unsigned long long any = 0;
+        if (edge) any = tree_seen_any(p, it.b, it.qn, lane) & tree_low_bits(it.qn);
+        bool odd = false;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          const int row = cw * 32 + (i >> 1) * 8 + (lane >> 3) * 2 + hi_row;
+          int c = (sub & 3) + 4 * (hi_row ^ (i & 1));
+          uint4 lo, hi;
+          if constexpr (KIND == TREE_INT4) {
+            c ^= ((lane >> 3) & 1) << 2;  // rows are 64 bytes: the next row pair takes the other half
+            const uint2 x = *reinterpret_cast<const uint2*>(raw + row * 64 + c * 8);
+            const uint32_t w4[4] = {x.x, x.y, 0u, 0u};
+            tree_widen<KIND>(w4, lo, hi);
+          } else {
+            const uint4 x = *reinterpret_cast<const uint4*>(raw + row * 128 + c * 16);
+            const uint32_t w4[4] = {x.x, x.y, x.z, x.w};
+            tree_widen<KIND>(w4, lo, hi);
+          }
+          if (edge) {
+            const int d = kv0 + row - base;  // draft index of this slot
+            if (d >= 0) {
+              if (d >= it.qn || !((any >> d) & 1)) {
+                lo = hi = make_uint4(0u, 0u, 0u, 0u);
+              } else if (KIND == TREE_FP8) {
+                uint32_t* wv[8] = {&lo.x, &lo.y, &lo.z, &lo.w, &hi.x, &hi.y, &hi.z, &hi.w};
+#pragma unroll
+                for (int k = 0; k < 8; ++k) odd |= bf16x2_drop_nonfinite(*wv[k]);
+              }
+            }
+          }
+          uint8_t* box = dst + (c >> 2) * C::BOX_BYTES;
+          const int ch = (c & 3) * 2;
+          *reinterpret_cast<uint4*>(box + sw128_offset(row, ch)) = lo;
+          *reinterpret_cast<uint4*>(box + sw128_offset(row, ch + 1)) = hi;
+        }
+        if (odd) odd_piece[qi & 7] = qi + 1;
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) {
+          mbar_arrive(&u_full[st]);
+          mbar_arrive(&raw_empty[rs]);
+        }
+        ++u;
+        return true;
+      };
+      // Scales of a tile: thread t loads those of token t one tile ahead.
+      float ks = 0.f, vs = 0.f;
+      auto fetch = [&](const TreePiece& it, int j) {
+        const int tok = (it.t0 + j) * 128 + t;
+        ks = vs = 0.f;
+        if (tok < it.len) {
+          const int pg = tree_page(p, it.b, tok);
+          if (pg >= 0) {
+            const long long row = ((long long)pg * p.page_size + tree_page_off(p, tok)) * p.Hkv + it.kvh;
+            ks = __ldg(p.k_scale + row);
+            vs = __ldg(p.v_scale + row);
+          }
+        }
+      };
+      auto scales = [&](const TreePiece& it, int j, bool prefetch) -> bool {
+        const int ss = g % C::NS;
+        if (!mbar_wait_warp<true>(&sc_empty[ss], ((g / C::NS) & 1) ^ 1, SITE_TR_CONV)) return false;
+        float* dst = reinterpret_cast<float*>(smem + C::OFF_SC) + ss * 256;
+        const int tok = (it.t0 + j) * 128 + t;
+        // A draft's scale may be anything; the rows that do not see it must not meet it.
+        if (tok >= it.len - it.qn && !(fabsf(vs) <= 3.4028234663852886e38f)) {
+          vs = 0.f;
+          if (tok < it.len) odd_piece[qi & 7] = qi + 1;
+        }
+        dst[t] = ks;
+        dst[128 + t] = vs;
+        if (prefetch) fetch(it, j + 1);
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&sc_full[ss]);
+        ++g;
+        return true;
+      };
+      TreeWalk w;
+      TreePiece it;
+      w.init(p, walk0);
+      while (ok && w.next(p, it)) {
+        const int n = it.n;
+        fetch(it, 0);
+        if constexpr (PAIR) {
+          for (int j = 0; j < n && ok; ++j)
+            ok = scales(it, j, j + 1 < n) && convert(it, j, false) && convert(it, j, true);
+        } else {
+          ok = scales(it, 0, n > 1) && convert(it, 0, false);
+          if (ok && n > 1) ok = scales(it, 1, n > 2) && convert(it, 1, false);
+          for (int j = 0; j < n && ok; ++j) {
+            ok = convert(it, j, true);
+            if (ok && j + 2 < n) ok = scales(it, j + 2, j + 3 < n) && convert(it, j + 2, false);
+          }
+        }
+        ++qi;
+      }
+    }
+  } else {
+    // ------------------------------------------------------------------ softmax + epilogue
+    regs_inc<C::REGS_SOFTMAX>();
+    const int slot = (warp - 4) >> 2;
+    const int wq = warp & 3;  // TMEM lane quarter this warp may access
+    const int r = wq * 32 + lane;
+    const uint32_t lane_off = (uint32_t)(wq * 32) << 16;
+    const uint32_t tS = tmem + slot * 128 + lane_off;
+    const uint32_t tO = tmem + 256 + slot * D + lane_off;
+    const int tok_i = (rb * C::NQ + (PAIR ? slot : 0)) * p.tps + r / p.G;  // this row's drafted token
+    const int head_g = r % p.G;
+    const bool row_used = r < p.tps * p.G && tok_i < p.n_q;
+    int cs = 0, g = 0, qi = 0, ub = 0;  // tiles of this slot, tiles of the CTA, pieces, units before this piece
+    bool ok = true;
+    TreeWalk w;
+    TreePiece it;
+    w.init(p, walk0);
+    while (ok && w.next(p, it)) {
+      const int n = it.n, base = it.len - it.qn;
+      const bool row_ok = row_used && tok_i < it.qn;
+      unsigned long long m64 = 0;
+      if (row_ok) m64 = (unsigned long long)__ldg(p.mask + (long long)it.b * p.n_q + tok_i) & tree_low_bits(it.qn);
+      float m_used = -INFINITY, l = 0.f;
+      for (int j = PAIR ? 0 : slot; j < n; j += PAIR ? 1 : 2) {
+        // tcgen05.ld/st are warp-collective: every lane takes the same branch around them.
+        if (!(ok = mbar_wait_warp<true>(&s_full[slot], cs & 1, SITE_TR_SM_S))) break;
+        tc_fence_after();
+        const int kv0 = (it.t0 + j) * 128;
+        const bool edge = kv0 + 128 > base;
+        uint32_t sr[128];
+#pragma unroll
+        for (int c = 0; c < 4; ++c) tmem_ld32(tS + c * 32, *reinterpret_cast<uint32_t(*)[32]>(&sr[c * 32]));
+        const float* sc = nullptr;
+        if constexpr (CODED) {
+          const int ss = (g + j) % C::NS;
+          if (!(ok = mbar_wait_warp<true>(&sc_full[ss], ((g + j) / C::NS) & 1, SITE_TR_SM_SC))) break;
+          sc = reinterpret_cast<const float*>(smem + C::OFF_SC) + ss * 256;
+        }
+#pragma unroll
+        for (int c = 0; c < 4; ++c) tmem_wait_ld_regs(*reinterpret_cast<uint32_t(*)[32]>(&sr[c * 32]));
+        if constexpr (CODED) {
+#pragma unroll
+          for (int i = 0; i < 128; i += 4) {
+            const float4 k4 = *reinterpret_cast<const float4*>(sc + i);
+            const float2 a = mul2(make_float2(__uint_as_float(sr[i]), __uint_as_float(sr[i + 1])),
+                                  make_float2(k4.x, k4.y));
+            const float2 b2 = mul2(make_float2(__uint_as_float(sr[i + 2]), __uint_as_float(sr[i + 3])),
+                                   make_float2(k4.z, k4.w));
+            sr[i] = __float_as_uint(a.x);
+            sr[i + 1] = __float_as_uint(a.y);
+            sr[i + 2] = __float_as_uint(b2.x);
+            sr[i + 3] = __float_as_uint(b2.y);
+          }
+        }
+        if (edge) {
+#pragma unroll
+          for (int c = 0; c < 4; ++c) {
+            const uint32_t see = tree_seen_word(c, kv0, base, m64);
+#pragma unroll
+            for (int i = 0; i < 32; ++i)
+              if (!((see >> i) & 1u)) sr[c * 32 + i] = __float_as_uint(-INFINITY);
+          }
+        }
+        float mx0 = -INFINITY, mx1 = -INFINITY, mx2 = -INFINITY, mx3 = -INFINITY;
+#pragma unroll
+        for (int i = 0; i < 128; i += 8) {
+          mx0 = max3(mx0, __uint_as_float(sr[i]), __uint_as_float(sr[i + 1]));
+          mx1 = max3(mx1, __uint_as_float(sr[i + 2]), __uint_as_float(sr[i + 3]));
+          mx2 = max3(mx2, __uint_as_float(sr[i + 4]), __uint_as_float(sr[i + 5]));
+          mx3 = max3(mx3, __uint_as_float(sr[i + 6]), __uint_as_float(sr[i + 7]));
+        }
+        const float m_tile = fmaxf(fmaxf(mx0, mx1), fmaxf(mx2, mx3)) * p.scale_log2;
+        const float m_new = fmaxf(m_used, m_tile);
+        const bool need = m_new > m_used + C::RESCALE_THRESHOLD;
+        if (__any_sync(0xffffffffu, need)) {
+          const float alpha = need ? ex2_approx(m_used - m_new) : 1.f;  // 0 when m_used = -inf
+          if (need) {
+            l *= alpha;
+            m_used = m_new;
+          }
+          if (j > (PAIR ? 0 : slot)) {  // the whole warp rescales its 32 rows of O (factor 1 where unchanged)
+#pragma unroll 1
+            for (int c = 0; c < D / 32; ++c) {
+              uint32_t orow[32];
+              tmem_ld32(tO + c * 32, orow);
+              tmem_wait_ld_regs(orow);
+#pragma unroll
+              for (int i = 0; i < 32; ++i) orow[i] = __float_as_uint(__uint_as_float(orow[i]) * alpha);
+              tmem_st32(tO + c * 32, orow);
+            }
+            tmem_wait_st();
+          }
+        }
+        const float neg_m = (m_used == -INFINITY) ? 0.f : -m_used;
+        const float2 c2 = make_float2(p.scale_log2, p.scale_log2);
+        const float2 nm2 = make_float2(neg_m, neg_m);
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+          uint32_t pk[16];
+#pragma unroll
+          for (int i = 0; i < 16; ++i) {
+            const int k = c * 32 + 2 * i;
+            const float2 x = fma2(make_float2(__uint_as_float(sr[k]), __uint_as_float(sr[k + 1])), c2, nm2);
+            float2 e;
+            e.x = ex2_approx(x.x);
+            e.y = ex2_approx(x.y);
+            sr[k] = __float_as_uint(e.x);
+            sr[k + 1] = __float_as_uint(e.y);
+            // One rounding of the weight to bf16 (at most 2^-8 of it, and the errors of different
+            // keys are independent), of its product with the V scale for a coded cache.
+            if constexpr (CODED) e = mul2(e, *reinterpret_cast<const float2*>(sc + 128 + k));
+            pk[i] = pack_bf16x2(e.x, e.y);
+          }
+          tmem_st16(tS + c * 16, pk);
+        }
+        tmem_wait_st();
+        if constexpr (!CODED) {
+          if (edge && (!PAIR || slot == 0)) {
+            // Thread r owns V row r of the tile: zero it if no token sees its slot, and its non-finite
+            // elements if some do.
+            const int vu = ub + tree_v_unit<PAIR>(j, n), st = vu % C::NU;
+            const unsigned long long any = tree_seen_any(p, it.b, it.qn, lane);
+            if (!(ok = mbar_wait_warp<true>(&u_full[st], (vu / C::NU) & 1, SITE_TR_SM_V))) break;
+            const int d = kv0 + r - base;
+            if (d >= 0) {
+              const bool drop = d >= it.qn || !((any >> d) & 1);
+              bool odd = false;
+#pragma unroll 1
+              for (int x = 0; x < C::NBOX * 8; ++x) {
+                uint4* q4 = reinterpret_cast<uint4*>(smem + C::OFF_U + st * C::TILE_BYTES + (x >> 3) * C::BOX_BYTES +
+                                                     r * 128 + (((x & 7) ^ (r & 7)) << 4));
+                uint4 v4 = make_uint4(0u, 0u, 0u, 0u);
+                bool bad = drop;
+                if (!drop) {
+                  v4 = *q4;
+                  bad |= bf16x2_drop_nonfinite(v4.x);
+                  bad |= bf16x2_drop_nonfinite(v4.y);
+                  bad |= bf16x2_drop_nonfinite(v4.z);
+                  bad |= bf16x2_drop_nonfinite(v4.w);
+                  odd |= bad;
+                }
+                if (bad) *q4 = v4;
+              }
+              if (odd) odd_piece[qi & 7] = qi + 1;
+            }
+            fence_proxy_async_smem();
+          }
+        }
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) {
+          mbar_arrive(&p_full[slot]);
+          if constexpr (CODED) mbar_arrive(&sc_empty[(g + j) % C::NS]);
+        }
+        {
+          float2 a0 = make_float2(0.f, 0.f), a1 = a0, a2 = a0, a3 = a0;
+#pragma unroll
+          for (int k = 0; k < 128; k += 8) {
+            a0 = add2(a0, make_float2(__uint_as_float(sr[k]), __uint_as_float(sr[k + 1])));
+            a1 = add2(a1, make_float2(__uint_as_float(sr[k + 2]), __uint_as_float(sr[k + 3])));
+            a2 = add2(a2, make_float2(__uint_as_float(sr[k + 4]), __uint_as_float(sr[k + 5])));
+            a3 = add2(a3, make_float2(__uint_as_float(sr[k + 6]), __uint_as_float(sr[k + 7])));
+          }
+          a0 = add2(add2(a0, a1), add2(a2, a3));
+          l += a0.x + a0.y;
+        }
+        ++cs;
+      }
+      if (!ok) break;
+      // ---- epilogue.  Weights of this slot's and the other half's O (PAIR: of this slot's alone).
+      float f_own, f_other = 0.f, lse2;
+      if constexpr (PAIR) {
+        f_own = l == 0.f ? 0.f : 1.f / l;
+        lse2 = l == 0.f ? -INFINITY : m_used + log2f(l);
+      } else {
+        float2* ml = reinterpret_cast<float2*>(smem + C::OFF_ML);
+        if (qi > 0 && !(ok = mbar_wait_warp<true>(ml_empty, (qi - 1) & 1, SITE_TR_EPI))) break;
+        ml[slot * 128 + r] = make_float2(m_used, l);
+        __syncwarp();
+        if (lane == 0) mbar_arrive(ml_full);
+        if (!(ok = mbar_wait_warp<true>(ml_full, qi & 1, SITE_TR_EPI))) break;
+        const float2 other = ml[(slot ^ 1) * 128 + r];
+        __syncwarp();
+        if (lane == 0) mbar_arrive(ml_empty);
+        const float m = fmaxf(m_used, other.x);  // a half without a visible key has m = -inf, l = 0
+        const float wa = l == 0.f ? 0.f : ex2_approx(m_used - m);
+        const float wb = other.y == 0.f ? 0.f : ex2_approx(other.x - m);
+        const float sum = l * wa + other.y * wb;
+        f_own = sum == 0.f ? 0.f : wa / sum;
+        f_other = sum == 0.f ? 0.f : wb / sum;
+        lse2 = sum == 0.f ? -INFINITY : m + log2f(sum);
+      }
+      if (!(ok = mbar_wait_warp<true>(o_full, qi & 1, SITE_TR_EPI))) break;
+      tc_fence_after();
+      const bool fix = *reinterpret_cast<volatile int*>(odd_piece + (qi & 7)) == qi + 1;
+      const long long orow = ((long long)it.b * p.n_q + tok_i) * p.Hq + (long long)it.kvh * p.G + head_g;
+      const long long prow = ((long long)blockIdx.x * 2 + it.which) * C::ROWS + (PAIR ? slot * 128 : 0) + r;
+      // PAIR: each slot stores its rows' D columns; halves: each slot stores half the columns of every row.
+      constexpr int NCH = PAIR ? D / 32 : D / 64;
+      const int ch0 = PAIR ? 0 : slot * NCH;
+#pragma unroll 1
+      for (int c = ch0; c < ch0 + NCH; ++c) {
+        uint32_t ov[32];
+        tmem_ld32(tO + c * 32, ov);
+        tmem_wait_ld_regs(ov);
+#pragma unroll
+        for (int i = 0; i < 32; ++i)  // an O that no PV wrote is not read into the sum
+          ov[i] = f_own == 0.f ? 0u : __float_as_uint(__uint_as_float(ov[i]) * f_own);
+        if constexpr (!PAIR) {
+          uint32_t o2[32];
+          tmem_ld32(tmem + 256 + (slot ^ 1) * D + lane_off + c * 32, o2);
+          tmem_wait_ld_regs(o2);
+#pragma unroll
+          for (int i = 0; i < 32; ++i)
+            if (f_other != 0.f)
+              ov[i] = __float_as_uint(fmaf(__uint_as_float(o2[i]), f_other, __uint_as_float(ov[i])));
+        }
+        if (c == ch0 + NCH - 1) {  // O has been read: the next piece's first PV may overwrite it
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(o_empty);
+        }
+        if (row_ok) {
+          if (fix && lse2 != -INFINITY) {  // non-finite values of the drafts this row sees
+#pragma unroll 1
+            for (int dq = 0; dq < it.qn; ++dq) {
+              const int tok = base + dq;
+              if (!((m64 >> dq) & 1) || tok < it.t0 * 128 || tok >= (it.t0 + n) * 128) continue;
+              const int pg = tree_page(p, it.b, tok);
+              if (pg < 0) continue;
+              const long long row = ((long long)pg * p.page_size + tree_page_off(p, tok)) * p.Hkv + it.kvh;
+#pragma unroll
+              for (int i = 0; i < 32; ++i) {
+                const float v = tree_v_value<KIND, D>(p, row, c * 32 + i);
+                if (!(fabsf(v) <= 3.4028234663852886e38f)) ov[i] = __float_as_uint(__uint_as_float(ov[i]) + v);
+              }
+            }
+          }
+          if (it.whole) {
+            uint4* dst = reinterpret_cast<uint4*>(p.o + orow * D + c * 32);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              uint4 x;
+              x.x = pack_bf16x2(__uint_as_float(ov[8 * i + 0]), __uint_as_float(ov[8 * i + 1]));
+              x.y = pack_bf16x2(__uint_as_float(ov[8 * i + 2]), __uint_as_float(ov[8 * i + 3]));
+              x.z = pack_bf16x2(__uint_as_float(ov[8 * i + 4]), __uint_as_float(ov[8 * i + 5]));
+              x.w = pack_bf16x2(__uint_as_float(ov[8 * i + 6]), __uint_as_float(ov[8 * i + 7]));
+              dst[i] = x;
+            }
+          } else {
+            float4* dst = reinterpret_cast<float4*>(p.part_o + prow * D + c * 32);
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+              dst[i] = make_float4(__uint_as_float(ov[4 * i]), __uint_as_float(ov[4 * i + 1]),
+                                   __uint_as_float(ov[4 * i + 2]), __uint_as_float(ov[4 * i + 3]));
+          }
+        }
+      }
+      if (row_ok && (PAIR || slot == 0)) {
+        if (!it.whole) p.part_lse[prow] = lse2;
+        else if (p.lse) p.lse[orow] = lse2 * 0.69314718055994531f;
+      }
+      g += n;
+      ub += 2 * n;
+      ++qi;
+    }
+  }
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 1) {
+    tc_fence_after();
+    tmem_dealloc(tmem, C::TMEM_COLS);
+  }
+}
+
+// Joins the partials of items that several CTAs shared, and writes the rows no tile belongs to.
+// One warp per row (sequence b, token i, head h); a row whose item one CTA finished is left alone.
+template <int D>
+__global__ void __launch_bounds__(256) tree_join_kernel(const TreeParams p, int rows_per_part, int slots) {
+  constexpr int V = D / 32;
+  const long long row = (long long)blockIdx.x * 8 + (threadIdx.x >> 5);
+  const int lane = threadIdx.x & 31;
+  if (row >= (long long)p.B * p.n_q * p.Hq) return;
+  const int h = (int)(row % p.Hq);
+  const long long bi = row / p.Hq;
+  const int i = (int)(bi % p.n_q), b = (int)(bi / p.n_q);
+  const int kvh = h / p.G, hg = h % p.G;
+  int total = 0, before = 0;
+  for (int x = lane; x < p.B; x += 32) {
+    const int n = tree_tiles(p, x);
+    total += n;
+    if (x < b) before += n;
+  }
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) {
+    total += __shfl_xor_sync(0xffffffffu, total, o);
+    before += __shfl_xor_sync(0xffffffffu, before, o);
+  }
+  const int tiles = tree_tiles(p, b);
+  float acc[V];
+#pragma unroll
+  for (int k = 0; k < V; ++k) acc[k] = 0.f;
+  float out = -INFINITY;
+  if (i < tree_qlen(p, b) && tiles > 0) {
+    const int W = total * p.Hkv, ng = min(p.n_groups, W);
+    const int a = before * p.Hkv + kvh * tiles;
+    const int g0 = (int)(((long long)(a + 1) * ng - 1) / W), g1 = (int)(((long long)(a + tiles) * ng - 1) / W);
+    if (g0 == g1) return;  // finished by its CTA
+    const int s = i / p.tps, rb = s / slots;
+    const int prow = (s % slots) * 128 + (i % p.tps) * p.G + hg;
+    auto part = [&](int g) -> long long {
+      const int which = g == g0 && a > tree_range(g0, W, ng) ? 1 : 0;
+      return (((long long)g * p.n_rb + rb) * 2 + which) * rows_per_part + prow;
+    };
+    float mx = -INFINITY;
+    bool nan = false;
+    for (int g = g0 + lane; g <= g1; g += 32) {
+      const float x = p.part_lse[part(g)];
+      nan |= x != x;
+      mx = fmaxf(mx, x);
+    }
+    mx = warp_max(mx);
+    if (__any_sync(0xffffffffu, nan)) mx = __int_as_float(0x7fc00000);
+    if (mx != -INFINITY) {
+      float sum = 0.f;
+      for (int g = g0 + lane; g <= g1; g += 32) sum += ex2_approx(p.part_lse[part(g)] - mx);
+      sum = warp_sum(sum);
+      out = (mx + log2f(sum)) * 0.69314718055994531f;
+      const float inv = 1.f / sum;
+#pragma unroll 4
+      for (int g = g0; g <= g1; ++g) {
+        const long long q = part(g);
+        const float lq = p.part_lse[q];
+        if (lq == -INFINITY) continue;
+        const float wgt = ex2_approx(lq - mx) * inv;
+        const float* src = p.part_o + q * D + lane * V;
+#pragma unroll
+        for (int k = 0; k < V; ++k) acc[k] = fmaf(wgt, src[k], acc[k]);
+      }
+    }
+  }
+  uint32_t* dst = reinterpret_cast<uint32_t*>(p.o + row * D + lane * V);
+#pragma unroll
+  for (int k = 0; k < V / 2; ++k) dst[k] = pack_bf16x2(acc[2 * k], acc[2 * k + 1]);
+  if (p.lse && lane == 0) p.lse[row] = out;
+}
+
+}  // namespace attn

@@ -222,6 +222,45 @@ ATTN_API attn_status_t attn_decode_paged(const void* q, const void* k_pool, cons
                                 int num_splits, void* o, float* lse, void* ws, size_t ws_bytes, void* stream);
 
 /* ------------------------------------------------------------------------------------------
+ * attn_decode_tree, attn_decode_tree_paged — verify a tree of drafted tokens in one cache pass.
+ *
+ * [ORT-QSA] Code analysis 2 (multi-token verification), for drafts that branch.  The cache already
+ * holds sequence b's q_lens[b] drafts as its last tokens.  With base = kv_lens[b] - q_lens[b],
+ * draft i sees cache slot t iff t < base, or base <= t < kv_lens[b] and bit (t - base) of the 64-bit
+ * word tree_mask[b, i] is set (bit i among them: a draft sees itself only if its own bit says so).
+ * A chain is mask[i] = 2^(i+1) - 1.  Rows i >= q_lens[b], and rows that see nothing, get O = 0,
+ * LSE = -inf.  Slots that no row sees are never used, whatever they hold; one that some rows see
+ * reaches those rows only (NaN and infinities included).
+ *
+ *   q, o       device bf16 [B, n_q, Hq, D], n_q <= 64;  lse device float32 [B, n_q, Hq] or NULL
+ *   k, v, k_scale, v_scale, page_table, page_size, num_pages, max_pages, kv_lens
+ *              as for attn_decode_splitkv / attn_decode_paged, for every cache type; lengths are
+ *              clamped to [0, Tmax], a base below 0 leaves slots [0, kv_lens[b]) as the drafts
+ *              -base, -base + 1, ...
+ *   q_lens     device int32 [B], each in [0, n_q], or NULL for n_q everywhere
+ *   tree_mask  device int64 [B, n_q], 8-byte aligned; bits at or past q_lens[b] are ignored
+ *   D          128, or 64 with a bf16 cache;  Hq / Hkv <= 128
+ *   ws         at least attn_decode_tree_workspace_bytes(dims, Tmax, n_q) bytes on the device that will
+ *              run the call (Tmax = max_pages * page_size when paged), 16-byte aligned, not shared by
+ *              calls that may overlap; may be NULL when that size is 0
+ * The work is cut into equal runs of 128-key tiles whatever the lengths, on the device: a captured
+ * call may be replayed with other lengths, masks and tables.  Results repeat bit for bit.
+ * A page-table entry outside [0, num_pages) reads as zeros and is reported by attn_device_status as
+ * ATTN_ERR_INVALID_ARG (site 60); the other sequences of the call, and later calls, are unaffected.
+ * Errors: as attn_decode_splitkv; ATTN_ERR_UNSUPPORTED for n_q > 64, other D and groups above 128.
+ * ------------------------------------------------------------------------------------------ */
+ATTN_API size_t attn_decode_tree_workspace_bytes(attn_dims_t dims, int Tmax, int n_q);
+ATTN_API attn_status_t attn_decode_tree(const void* q, const void* k, const void* v, attn_dtype_t kv_dtype,
+                               const float* k_scale, const float* v_scale, const int* kv_lens, const int* q_lens,
+                               const long long* tree_mask, int Tmax, int n_q, attn_dims_t dims, void* o, float* lse,
+                               void* ws, size_t ws_bytes, void* stream);
+ATTN_API attn_status_t attn_decode_tree_paged(const void* q, const void* k_pool, const void* v_pool,
+                               attn_dtype_t kv_dtype, const float* k_scale_pool, const float* v_scale_pool,
+                               const int* page_table, int max_pages, int page_size, int num_pages, const int* kv_lens,
+                               const int* q_lens, const long long* tree_mask, int n_q, attn_dims_t dims, void* o,
+                               float* lse, void* ws, size_t ws_bytes, void* stream);
+
+/* ------------------------------------------------------------------------------------------
  * attn_decode_splitkv_noalloc — the same split-KV decode, for callers that cannot allocate.
  *
  * The pages have no counterpart to this entry point; it is an integration aid.  Some callers
@@ -329,7 +368,7 @@ ATTN_API const char* attn_status_string(attn_status_t status);
 ATTN_API int attn_last_cuda_error(void);
 /* Reads the device status word of the current device (synchronises the device).  Returns
  * ATTN_ERR_TIMEOUT if a kernel's bounded wait ran out since the last reset, ATTN_ERR_INVALID_ARG
- * if a decode kernel met a page-table entry outside the pool, and stores the site in *site when
+ * if a kernel met a page-table entry outside the pool or another bad value among its device arguments, and stores the site in *site when
  * site != NULL.  reset != 0 clears the word. */
 ATTN_API attn_status_t attn_device_status(int reset, int* site);
 /* Upper bound of any single in-kernel wait, in nanoseconds (default 2e9). */
