@@ -206,12 +206,12 @@ struct TreeCfg {
   static constexpr int N_BARS = 2 + 2 * NU + 2 * NR + 2 * NS + 2 + 2 + 2 + 2 + 1;
   static constexpr int SMEM_BYTES = OFF_BAR + N_BARS * 8 + 64 + 1024;  // + walk start, flags, alignment slack
   static constexpr int THREADS = CODED ? 512 : 384;
-  // Register split: control warpgroup, converter warpgroup, two softmax warpgroups; the sum never
-  // exceeds what the launch holds (checked on the host before the first launch).
-  static constexpr int REGS_CTRL = CODED ? 64 : 72;
-  static constexpr int REGS_CONV = 80;
-  static constexpr int REGS_SOFTMAX = CODED ? 184 : 216;
-  static constexpr int REGS_TOTAL = REGS_CTRL * 128 + (CODED ? REGS_CONV * 128 : 0) + REGS_SOFTMAX * 256;
+  // bf16: the softmax holds a row's 128 scores in registers; the control warpgroup gives up what that
+  // takes (the sum never exceeds what the launch holds: checked on the host before the first launch).
+  // Coded caches need no split: there the softmax reads the scores from TMEM twice, 32 at a time.
+  static constexpr int REGS_CTRL = 72;
+  static constexpr int REGS_SOFTMAX = 216;
+  static constexpr int REGS_TOTAL = CODED ? 0 : REGS_CTRL * 128 + REGS_SOFTMAX * 256;
   static constexpr uint32_t TMEM_COLS = 512;
   static constexpr float RESCALE_THRESHOLD = 8.0f;
   static constexpr int ROWS = PAIR ? 256 : 128;  // rows of a partial
@@ -290,6 +290,28 @@ __device__ __forceinline__ bool bf16x2_drop_nonfinite(uint32_t& w) {
     bad = true;
   }
   return bad;
+}
+
+// Row r of an MMA-ready V tile: zeros when drop, else its non-finite elements set to zero (true if any).
+template <int NBOX>
+__device__ __forceinline__ bool tree_scrub_row(uint8_t* tile, int r, bool drop) {
+  bool odd = false;
+#pragma unroll 1
+  for (int x = 0; x < NBOX * 8; ++x) {
+    uint4* q4 = reinterpret_cast<uint4*>(tile + (x >> 3) * (128 * 128) + sw128_offset(r, x & 7));
+    uint4 v4 = make_uint4(0u, 0u, 0u, 0u);
+    bool bad = drop;
+    if (!drop) {
+      v4 = *q4;
+      bad |= bf16x2_drop_nonfinite(v4.x);
+      bad |= bf16x2_drop_nonfinite(v4.y);
+      bad |= bf16x2_drop_nonfinite(v4.z);
+      bad |= bf16x2_drop_nonfinite(v4.w);
+      odd |= bad;
+    }
+    if (bad) *q4 = v4;
+  }
+  return odd;
 }
 
 // One V element of the cache as float (the epilogue's slow path).
@@ -412,7 +434,7 @@ __global__ void __launch_bounds__((TreeCfg<KIND, D, PAIR>::THREADS), 1)
 
   if (warp == 0) {
     // ------------------------------------------------------------------ TMA producer
-    regs_dec<C::REGS_CTRL>();
+    if constexpr (!CODED) regs_dec<C::REGS_CTRL>();
     if (lane == 0) {
       tma_prefetch_desc(&tmQ);
       tma_prefetch_desc(&tmK);
@@ -473,7 +495,7 @@ __global__ void __launch_bounds__((TreeCfg<KIND, D, PAIR>::THREADS), 1)
     __syncwarp();
   } else if (warp == 1) {
     // ------------------------------------------------------------------ MMA issuer
-    regs_dec<C::REGS_CTRL>();
+    if constexpr (!CODED) regs_dec<C::REGS_CTRL>();
     {
       constexpr uint32_t idesc_qk = make_idesc_f16(128, 128, false, false, true);
       constexpr uint32_t idesc_pv = make_idesc_f16(128, D, false, true, true);
@@ -590,16 +612,18 @@ __global__ void __launch_bounds__((TreeCfg<KIND, D, PAIR>::THREADS), 1)
     }
     __syncwarp();
   } else if (warp < 4) {
-    regs_dec<C::REGS_CTRL>();
+    if constexpr (!CODED) regs_dec<C::REGS_CTRL>();
   } else if (CODED && warp >= 12) {
     // ------------------------------------------------------------------ converters
     if constexpr (CODED) {
-      regs_dec<C::REGS_CONV>();
       const int cw = warp - 12, t = cw * 32 + lane;
       // Lane l of a warp widens 16 codes: row pair 2 (l >> 3) + ((l >> 2) & 1) of eight rows, 16-code column c.  The
       // two rows of a pair take columns 0-3 and 4-7, so the eight lanes of a phase read 128 distinct
       // bytes and their two 16-byte results go to eight distinct chunks of the swizzled tile.
+      // One rolled copy of this code serves K and V: unrolled per unit kind it overflowed the instruction
+      // cache (4.3 of 17 stall cycles an instruction, 8400 cycles a tile against 1450 of HBM time).
       const int sub = lane & 7, hi_row = sub >> 2;
+      const int row0 = cw * 32 + (lane >> 3) * 2 + hi_row;
       int u = 0, g = 0, qi = 0;
       bool ok = true;
       auto convert = [&](const TreePiece& it, int j, bool is_v) -> bool {
@@ -609,44 +633,44 @@ __global__ void __launch_bounds__((TreeCfg<KIND, D, PAIR>::THREADS), 1)
         if (!r) return false;
         const uint8_t* raw = smem + C::OFF_RAW + rs * C::RAW_BYTES;
         uint8_t* dst = smem + C::OFF_U + st * C::TILE_BYTES;
-        const int kv0 = (it.t0 + j) * 128, base = it.len - it.qn;
-        const bool edge = is_v && kv0 + 128 > base;
-        unsigned long long any = 0;
-        if (edge) any = tree_seen_any(p, it.b, it.qn, lane) & tree_low_bits(it.qn);
-        bool odd = false;
+#pragma unroll 1
+        for (int h = 0; h < 2; ++h) {
+          uint32_t w4[4][4];
+          int col[4];
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          const int row = cw * 32 + (i >> 1) * 8 + (lane >> 3) * 2 + hi_row;
-          int c = (sub & 3) + 4 * (hi_row ^ (i & 1));
-          uint4 lo, hi;
-          if constexpr (KIND == TREE_INT4) {
-            c ^= ((lane >> 3) & 1) << 2;  // rows are 64 bytes: the next row pair takes the other half
-            const uint2 x = *reinterpret_cast<const uint2*>(raw + row * 64 + c * 8);
-            const uint32_t w4[4] = {x.x, x.y, 0u, 0u};
-            tree_widen<KIND>(w4, lo, hi);
-          } else {
-            const uint4 x = *reinterpret_cast<const uint4*>(raw + row * 128 + c * 16);
-            const uint32_t w4[4] = {x.x, x.y, x.z, x.w};
-            tree_widen<KIND>(w4, lo, hi);
-          }
-          if (edge) {
-            const int d = kv0 + row - base;  // draft index of this slot
-            if (d >= 0) {
-              if (d >= it.qn || !((any >> d) & 1)) {
-                lo = hi = make_uint4(0u, 0u, 0u, 0u);
-              } else if (KIND == TREE_FP8) {
-                uint32_t* wv[8] = {&lo.x, &lo.y, &lo.z, &lo.w, &hi.x, &hi.y, &hi.z, &hi.w};
-#pragma unroll
-                for (int k = 0; k < 8; ++k) odd |= bf16x2_drop_nonfinite(*wv[k]);
-              }
+          for (int i = 0; i < 4; ++i) {  // rows row0 + 16 h + 8 (i >> 1), both halves of their columns
+            const int row = row0 + h * 16 + (i >> 1) * 8;
+            col[i] = (sub & 3) + 4 * (hi_row ^ (i & 1));
+            if constexpr (KIND == TREE_INT4) {
+              col[i] ^= ((lane >> 3) & 1) << 2;  // rows are 64 bytes: the next row pair takes the other half
+              const uint2 x = *reinterpret_cast<const uint2*>(raw + row * 64 + col[i] * 8);
+              w4[i][0] = x.x, w4[i][1] = x.y, w4[i][2] = w4[i][3] = 0u;
+            } else {
+              const uint4 x = *reinterpret_cast<const uint4*>(raw + row * 128 + col[i] * 16);
+              w4[i][0] = x.x, w4[i][1] = x.y, w4[i][2] = x.z, w4[i][3] = x.w;
             }
           }
-          uint8_t* box = dst + (c >> 2) * C::BOX_BYTES;
-          const int ch = (c & 3) * 2;
-          *reinterpret_cast<uint4*>(box + sw128_offset(row, ch)) = lo;
-          *reinterpret_cast<uint4*>(box + sw128_offset(row, ch + 1)) = hi;
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            uint4 lo, hi;
+            tree_widen<KIND>(w4[i], lo, hi);
+            const int row = row0 + h * 16 + (i >> 1) * 8;
+            uint8_t* box = dst + (col[i] >> 2) * C::BOX_BYTES;
+            const int ch = (col[i] & 3) * 2;
+            *reinterpret_cast<uint4*>(box + sw128_offset(row, ch)) = lo;
+            *reinterpret_cast<uint4*>(box + sw128_offset(row, ch + 1)) = hi;
+          }
         }
-        if (odd) odd_piece[qi & 7] = qi + 1;
+        const int kv0 = (it.t0 + j) * 128, base = it.len - it.qn;
+        if (is_v && kv0 + 128 > base) {  // this warp's rows that are drafts, or past them
+          const unsigned long long any = tree_seen_any(p, it.b, it.qn, lane);
+          const int d = kv0 + t - base;
+          __syncwarp();
+          if (d >= 0) {
+            const bool drop = d >= it.qn || !((any >> d) & 1);
+            if (tree_scrub_row<C::NBOX>(dst, t, drop)) odd_piece[qi & 7] = qi + 1;
+          }
+        }
         fence_proxy_async_smem();
         __syncwarp();
         if (lane == 0) {
@@ -680,7 +704,7 @@ __global__ void __launch_bounds__((TreeCfg<KIND, D, PAIR>::THREADS), 1)
           vs = 0.f;
           if (tok < it.len) odd_piece[qi & 7] = qi + 1;
         }
-        dst[t] = ks;
+        dst[t] = ks * p.scale_log2;
         dst[128 + t] = vs;
         if (prefetch) fetch(it, j + 1);
         __syncwarp();
@@ -694,23 +718,25 @@ __global__ void __launch_bounds__((TreeCfg<KIND, D, PAIR>::THREADS), 1)
       while (ok && w.next(p, it)) {
         const int n = it.n;
         fetch(it, 0);
-        if constexpr (PAIR) {
-          for (int j = 0; j < n && ok; ++j)
-            ok = scales(it, j, j + 1 < n) && convert(it, j, false) && convert(it, j, true);
-        } else {
-          ok = scales(it, 0, n > 1) && convert(it, 0, false);
-          if (ok && n > 1) ok = scales(it, 1, n > 2) && convert(it, 1, false);
-          for (int j = 0; j < n && ok; ++j) {
-            ok = convert(it, j, true);
-            if (ok && j + 2 < n) ok = scales(it, j + 2, j + 3 < n) && convert(it, j + 2, false);
+        for (int x = 0; x < 2 * n && ok; ++x) {  // the units of the piece, in the order of tree_v_unit
+          bool is_v;
+          int j;
+          if constexpr (PAIR) {
+            is_v = x & 1;
+            j = x >> 1;
+          } else {
+            is_v = x == 2 * n - 1 || (x > 0 && !(x & 1));
+            j = x == 2 * n - 1 ? n - 1 : is_v ? (x - 2) >> 1 : (x + 1) >> 1;
           }
+          if (!is_v) ok = scales(it, j, j + 1 < n);
+          ok = ok && convert(it, j, is_v);
         }
         ++qi;
       }
     }
   } else {
     // ------------------------------------------------------------------ softmax + epilogue
-    regs_inc<C::REGS_SOFTMAX>();
+    if constexpr (!CODED) regs_inc<C::REGS_SOFTMAX>();
     const int slot = (warp - 4) >> 2;
     const int wq = warp & 3;  // TMEM lane quarter this warp may access
     const int r = wq * 32 + lane;
@@ -737,49 +763,67 @@ __global__ void __launch_bounds__((TreeCfg<KIND, D, PAIR>::THREADS), 1)
         tc_fence_after();
         const int kv0 = (it.t0 + j) * 128;
         const bool edge = kv0 + 128 > base;
-        uint32_t sr[128];
+        // bf16: sr holds the row's 128 scores; coded caches: two chunks of 32, chunk c in sr + 32 (c & 1).
+        uint32_t sr[CODED ? 64 : 128];
+        auto chunk = [&](int c) -> uint32_t(&)[32] { return *reinterpret_cast<uint32_t(*)[32]>(&sr[(CODED ? c & 1 : c) * 32]); };
+        auto mask_chunk = [&](int c, uint32_t(&x)[32]) {
+          const uint32_t see = tree_seen_word(c, kv0, base, m64);
 #pragma unroll
-        for (int c = 0; c < 4; ++c) tmem_ld32(tS + c * 32, *reinterpret_cast<uint32_t(*)[32]>(&sr[c * 32]));
+          for (int i = 0; i < 32; ++i)
+            if (!((see >> i) & 1u)) x[i] = __float_as_uint(-INFINITY);
+        };
         const float* sc = nullptr;
+        float mx0 = -INFINITY, mx1 = -INFINITY, mx2 = -INFINITY, mx3 = -INFINITY;
         if constexpr (CODED) {
           const int ss = (g + j) % C::NS;
           if (!(ok = mbar_wait_warp<true>(&sc_full[ss], ((g + j) / C::NS) & 1, SITE_TR_SM_SC))) break;
+          tmem_ld32(tS, chunk(0));
           sc = reinterpret_cast<const float*>(smem + C::OFF_SC) + ss * 256;
-        }
-#pragma unroll
-        for (int c = 0; c < 4; ++c) tmem_wait_ld_regs(*reinterpret_cast<uint32_t(*)[32]>(&sr[c * 32]));
-        if constexpr (CODED) {
-#pragma unroll
-          for (int i = 0; i < 128; i += 4) {
-            const float4 k4 = *reinterpret_cast<const float4*>(sc + i);
-            const float2 a = mul2(make_float2(__uint_as_float(sr[i]), __uint_as_float(sr[i + 1])),
-                                  make_float2(k4.x, k4.y));
-            const float2 b2 = mul2(make_float2(__uint_as_float(sr[i + 2]), __uint_as_float(sr[i + 3])),
-                                   make_float2(k4.z, k4.w));
-            sr[i] = __float_as_uint(a.x);
-            sr[i + 1] = __float_as_uint(a.y);
-            sr[i + 2] = __float_as_uint(b2.x);
-            sr[i + 3] = __float_as_uint(b2.y);
-          }
-        }
-        if (edge) {
-#pragma unroll
+#pragma unroll 2
           for (int c = 0; c < 4; ++c) {
-            const uint32_t see = tree_seen_word(c, kv0, base, m64);
+            uint32_t(&x)[32] = chunk(c);
+            tmem_wait_ld_regs(x);
+            tmem_ld32(tS + ((c + 1) & 3) * 32, chunk(c + 1));  // after the last, chunk 0 again for the weights
 #pragma unroll
-            for (int i = 0; i < 32; ++i)
-              if (!((see >> i) & 1u)) sr[c * 32 + i] = __float_as_uint(-INFINITY);
+            for (int i = 0; i < 32; i += 4) {
+              const float4 k4 = *reinterpret_cast<const float4*>(sc + c * 32 + i);
+              const float2 a = mul2(make_float2(__uint_as_float(x[i]), __uint_as_float(x[i + 1])),
+                                    make_float2(k4.x, k4.y));
+              const float2 b2 = mul2(make_float2(__uint_as_float(x[i + 2]), __uint_as_float(x[i + 3])),
+                                     make_float2(k4.z, k4.w));
+              x[i] = __float_as_uint(a.x);
+              x[i + 1] = __float_as_uint(a.y);
+              x[i + 2] = __float_as_uint(b2.x);
+              x[i + 3] = __float_as_uint(b2.y);
+            }
+            if (edge) mask_chunk(c, x);
+#pragma unroll
+            for (int i = 0; i < 32; i += 8) {
+              mx0 = max3(mx0, __uint_as_float(x[i]), __uint_as_float(x[i + 1]));
+              mx1 = max3(mx1, __uint_as_float(x[i + 2]), __uint_as_float(x[i + 3]));
+              mx2 = max3(mx2, __uint_as_float(x[i + 4]), __uint_as_float(x[i + 5]));
+              mx3 = max3(mx3, __uint_as_float(x[i + 6]), __uint_as_float(x[i + 7]));
+            }
+          }
+        } else {
+#pragma unroll
+          for (int c = 0; c < 4; ++c) tmem_ld32(tS + c * 32, chunk(c));
+#pragma unroll
+          for (int c = 0; c < 4; ++c) tmem_wait_ld_regs(chunk(c));
+          if (edge) {
+#pragma unroll
+            for (int c = 0; c < 4; ++c) mask_chunk(c, chunk(c));
+          }
+#pragma unroll
+          for (int i = 0; i < 128; i += 8) {
+            mx0 = max3(mx0, __uint_as_float(sr[i]), __uint_as_float(sr[i + 1]));
+            mx1 = max3(mx1, __uint_as_float(sr[i + 2]), __uint_as_float(sr[i + 3]));
+            mx2 = max3(mx2, __uint_as_float(sr[i + 4]), __uint_as_float(sr[i + 5]));
+            mx3 = max3(mx3, __uint_as_float(sr[i + 6]), __uint_as_float(sr[i + 7]));
           }
         }
-        float mx0 = -INFINITY, mx1 = -INFINITY, mx2 = -INFINITY, mx3 = -INFINITY;
-#pragma unroll
-        for (int i = 0; i < 128; i += 8) {
-          mx0 = max3(mx0, __uint_as_float(sr[i]), __uint_as_float(sr[i + 1]));
-          mx1 = max3(mx1, __uint_as_float(sr[i + 2]), __uint_as_float(sr[i + 3]));
-          mx2 = max3(mx2, __uint_as_float(sr[i + 4]), __uint_as_float(sr[i + 5]));
-          mx3 = max3(mx3, __uint_as_float(sr[i + 6]), __uint_as_float(sr[i + 7]));
-        }
-        const float m_tile = fmaxf(fmaxf(mx0, mx1), fmaxf(mx2, mx3)) * p.scale_log2;
+        // Scores in units of log2: the staged K scales of a coded cache hold the factor already.
+        const float m_tile = fmaxf(fmaxf(mx0, mx1), fmaxf(mx2, mx3)) * (CODED ? 1.f : p.scale_log2);
         const float m_new = fmaxf(m_used, m_tile);
         const bool need = m_new > m_used + C::RESCALE_THRESHOLD;
         if (__any_sync(0xffffffffu, need)) {
@@ -804,21 +848,43 @@ __global__ void __launch_bounds__((TreeCfg<KIND, D, PAIR>::THREADS), 1)
         const float neg_m = (m_used == -INFINITY) ? 0.f : -m_used;
         const float2 c2 = make_float2(p.scale_log2, p.scale_log2);
         const float2 nm2 = make_float2(neg_m, neg_m);
-#pragma unroll
+        float2 a0 = make_float2(0.f, 0.f), a1 = a0, a2 = a0, a3 = a0;  // the row sum, of the unrounded weights
+        auto add_sum = [&](int i, float2 e) {
+          float2& a = (i & 3) == 0 ? a0 : (i & 3) == 1 ? a1 : (i & 3) == 2 ? a2 : a3;
+          a = add2(a, e);
+        };
+#pragma unroll(CODED ? 2 : 4)
         for (int c = 0; c < 4; ++c) {
           uint32_t pk[16];
+          uint32_t(&x)[32] = chunk(c);
+          if constexpr (CODED) {
+            tmem_wait_ld_regs(x);
+            // P lands in columns 16 c .. 16 c + 15, all below the chunk that is still to be read.
+            if (c < 3) tmem_ld32(tS + (c + 1) * 32, chunk(c + 1));
+          }
+          uint32_t see = ~0u;
+          if (CODED && edge) see = tree_seen_word(c, kv0, base, m64);
 #pragma unroll
           for (int i = 0; i < 16; ++i) {
             const int k = c * 32 + 2 * i;
-            const float2 x = fma2(make_float2(__uint_as_float(sr[k]), __uint_as_float(sr[k + 1])), c2, nm2);
+            float2 y = make_float2(__uint_as_float(x[2 * i]), __uint_as_float(x[2 * i + 1]));
+            y = fma2(y, CODED ? *reinterpret_cast<const float2*>(sc + k) : c2, nm2);
             float2 e;
-            e.x = ex2_approx(x.x);
-            e.y = ex2_approx(x.y);
-            sr[k] = __float_as_uint(e.x);
-            sr[k + 1] = __float_as_uint(e.y);
+            e.x = ex2_approx(y.x);
+            e.y = ex2_approx(y.y);
+            if (CODED && edge) {
+              if (!((see >> (2 * i)) & 1u)) e.x = 0.f;
+              if (!((see >> (2 * i + 1)) & 1u)) e.y = 0.f;
+            }
             // One rounding of the weight to bf16 (at most 2^-8 of it, and the errors of different
             // keys are independent), of its product with the V scale for a coded cache.
-            if constexpr (CODED) e = mul2(e, *reinterpret_cast<const float2*>(sc + 128 + k));
+            if constexpr (CODED) {
+              add_sum(i, e);
+              e = mul2(e, *reinterpret_cast<const float2*>(sc + 128 + k));
+            } else {
+              x[2 * i] = __float_as_uint(e.x);
+              x[2 * i + 1] = __float_as_uint(e.y);
+            }
             pk[i] = pack_bf16x2(e.x, e.y);
           }
           tmem_st16(tS + c * 16, pk);
@@ -834,24 +900,7 @@ __global__ void __launch_bounds__((TreeCfg<KIND, D, PAIR>::THREADS), 1)
             const int d = kv0 + r - base;
             if (d >= 0) {
               const bool drop = d >= it.qn || !((any >> d) & 1);
-              bool odd = false;
-#pragma unroll 1
-              for (int x = 0; x < C::NBOX * 8; ++x) {
-                uint4* q4 = reinterpret_cast<uint4*>(smem + C::OFF_U + st * C::TILE_BYTES + (x >> 3) * C::BOX_BYTES +
-                                                     r * 128 + (((x & 7) ^ (r & 7)) << 4));
-                uint4 v4 = make_uint4(0u, 0u, 0u, 0u);
-                bool bad = drop;
-                if (!drop) {
-                  v4 = *q4;
-                  bad |= bf16x2_drop_nonfinite(v4.x);
-                  bad |= bf16x2_drop_nonfinite(v4.y);
-                  bad |= bf16x2_drop_nonfinite(v4.z);
-                  bad |= bf16x2_drop_nonfinite(v4.w);
-                  odd |= bad;
-                }
-                if (bad) *q4 = v4;
-              }
-              if (odd) odd_piece[qi & 7] = qi + 1;
+              if (tree_scrub_row<C::NBOX>(smem + C::OFF_U + st * C::TILE_BYTES, r, drop)) odd_piece[qi & 7] = qi + 1;
             }
             fence_proxy_async_smem();
           }
@@ -862,18 +911,13 @@ __global__ void __launch_bounds__((TreeCfg<KIND, D, PAIR>::THREADS), 1)
           mbar_arrive(&p_full[slot]);
           if constexpr (CODED) mbar_arrive(&sc_empty[(g + j) % C::NS]);
         }
-        {
-          float2 a0 = make_float2(0.f, 0.f), a1 = a0, a2 = a0, a3 = a0;
+        if constexpr (!CODED) {  // after P is handed over: the MMA does not wait for it
 #pragma unroll
-          for (int k = 0; k < 128; k += 8) {
-            a0 = add2(a0, make_float2(__uint_as_float(sr[k]), __uint_as_float(sr[k + 1])));
-            a1 = add2(a1, make_float2(__uint_as_float(sr[k + 2]), __uint_as_float(sr[k + 3])));
-            a2 = add2(a2, make_float2(__uint_as_float(sr[k + 4]), __uint_as_float(sr[k + 5])));
-            a3 = add2(a3, make_float2(__uint_as_float(sr[k + 6]), __uint_as_float(sr[k + 7])));
-          }
-          a0 = add2(add2(a0, a1), add2(a2, a3));
-          l += a0.x + a0.y;
+          for (int i = 0; i < 64; ++i)
+            add_sum(i, make_float2(__uint_as_float(sr[2 * i]), __uint_as_float(sr[2 * i + 1])));
         }
+        a0 = add2(add2(a0, a1), add2(a2, a3));
+        l += a0.x + a0.y;
         ++cs;
       }
       if (!ok) break;
