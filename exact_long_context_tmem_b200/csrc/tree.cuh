@@ -24,15 +24,21 @@
 //
 // Pipeline, as the prefill's: S = Q K^T in TMEM, one thread per row for the softmax, P (bf16) over S,
 // O += P V; unit ring of MMA-ready K and V tiles in consumption order.  Coded caches (E4M3, INT8, INT4)
-// land raw in a ring of their own and a fourth warpgroup widens them to bf16, which is exact for
-// every code; the K scale multiplies the fp32 score and the V scale the fp32 weight before its one
-// rounding to bf16, so no scale is rounded.
+// land raw in a ring of their own and a fourth warpgroup widens them to f16, which is exact for
+// every code (one instruction per two E4M3 codes, five per four INT8 codes; bf16 took five and eight);
+// the queries follow as f16 times a power of two.  The K scale multiplies the fp32 score and the V
+// scale the fp32 weight before its one rounding to f16, so no scale is rounded.  A row's weights are
+// taken relative to its largest weight times V scale, max_t (y_t + log2 |v_scale_t|), not to its largest weight:
+// the products are at most 2^8 and the large ones keep f16's full precision whatever the scales.
 //
 // Masked places.  Slots past kv_len and drafts no token sees are never used.  A draft that some tokens
 // see may hold anything too: its non-finite V elements enter the MMA as zeros (0 * NaN would reach
 // the rows that do not see it) and the epilogue adds them back to the rows that do.
 #pragma once
 
+#include <type_traits>
+
+#include "decode_int.cuh"
 #include "ptx.cuh"
 
 namespace attn {
@@ -200,10 +206,11 @@ struct TreeCfg {
   static constexpr int OFF_Q = 0;
   static constexpr int OFF_U = OFF_Q + NQ * TILE_BYTES;
   static constexpr int OFF_RAW = OFF_U + NU * TILE_BYTES;
-  static constexpr int OFF_SC = OFF_RAW + NR * RAW_BYTES;      // [NS][2][128] floats
-  static constexpr int OFF_ML = OFF_SC + NS * 1024;            // [2 slots][128] (max, sum) of the halves
-  static constexpr int OFF_BAR = OFF_ML + (PAIR ? 0 : 2048);
-  static constexpr int N_BARS = 2 + 2 * NU + 2 * NR + 2 * NS + 2 + 2 + 2 + 2 + 1;
+  static constexpr int OFF_SC = OFF_RAW + NR * RAW_BYTES;      // [NS][3][128] floats
+  static constexpr int OFF_ML = OFF_SC + NS * 1536;            // [2 slots][128] (max, sum) of the halves
+  static constexpr int OFF_WALK = OFF_ML + (PAIR ? 0 : 2048);  // [8] walks, [8] pieces of the softmax warps
+  static constexpr int OFF_BAR = OFF_WALK + 8 * (int)(sizeof(TreeWalk) + sizeof(TreePiece));
+  static constexpr int N_BARS = 3 + 2 * NU + 2 * NR + 2 * NS + 2 + 2 + 2 + 2 + 1;
   static constexpr int SMEM_BYTES = OFF_BAR + N_BARS * 8 + 64 + 1024;  // + walk start, flags, alignment slack
   static constexpr int THREADS = CODED ? 512 : 384;
   // bf16: the softmax holds a row's 128 scores in registers; the control warpgroup gives up what that
@@ -212,6 +219,8 @@ struct TreeCfg {
   static constexpr int REGS_CTRL = 72;
   static constexpr int REGS_SOFTMAX = 216;
   static constexpr int REGS_TOTAL = CODED ? 0 : REGS_CTRL * 128 + REGS_SOFTMAX * 256;
+  static constexpr uint32_t EXP_MASK = CODED ? 0x7c00u : 0x7f80u;  // exponent field of an MMA operand
+  static constexpr int SC_BYTES = 3 * 512;  // scales of a tile: K (times all score factors), V, log2 |V|
   static constexpr uint32_t TMEM_COLS = 512;
   static constexpr float RESCALE_THRESHOLD = 8.0f;
   static constexpr int ROWS = PAIR ? 256 : 128;  // rows of a partial
@@ -224,68 +233,43 @@ __device__ __forceinline__ int tree_v_unit(int j, int n) {
   return PAIR ? 2 * j + 1 : min(j + 2, n) + j;
 }
 
-// Two codes (16 bits, first in the low byte) -> two bf16, exact.
-__device__ __forceinline__ uint32_t e4m3x2_to_bf16x2(uint16_t c) {
-  const uint32_t h = e4m3x2_to_f16x2(c);
-  const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&h));
-  return pack_bf16x2(f.x, f.y);
-}
-__device__ __forceinline__ uint32_t bf16x2_sub(uint32_t a, uint32_t b) {
-  uint32_t r;
-  asm("sub.rn.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
-  return r;
-}
-// INT8: the code c in byte form is 7 value bits u and a sign bit s, c = u - 128 s.  0x4300 | u is the bf16
-// 128 + u (one unit in the last place is 1 there) and 0x4300 | (s << 7) is 128 or 256, so their
-// difference is c exactly.
-__device__ __forceinline__ uint32_t int8x2_to_bf16x2(uint32_t w, uint32_t sel) {
-  uint32_t v;
-  asm("prmt.b32 %0, %1, 0, %2;" : "=r"(v) : "r"(w), "r"(sel));  // codes in the low bytes of two 16-bit lanes
-  return bf16x2_sub((v & 0x007f007fu) | 0x43004300u, (v & 0x00800080u) | 0x43004300u);
-}
-
-// 16 raw codes -> 32 bytes of bf16 (two 16-byte chunks).
+// 16 raw codes -> 32 bytes of f16 (two 16-byte chunks), exact.  INT4 groups of eight come out in the order of
+// i4x8_to_f16_paired; the queries take the same order, and the epilogue undoes it for V.
 template <int KIND>
 __device__ __forceinline__ void tree_widen(const uint32_t (&w)[4], uint4& lo, uint4& hi) {
   uint32_t r[8];
   if constexpr (KIND == TREE_FP8) {
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-      r[2 * i] = e4m3x2_to_bf16x2((uint16_t)(w[i] & 0xffffu));
-      r[2 * i + 1] = e4m3x2_to_bf16x2((uint16_t)(w[i] >> 16));
+      r[2 * i] = e4m3x2_to_f16x2((uint16_t)(w[i] & 0xffffu));
+      r[2 * i + 1] = e4m3x2_to_f16x2((uint16_t)(w[i] >> 16));
     }
   } else if constexpr (KIND == TREE_INT8) {
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      r[2 * i] = int8x2_to_bf16x2(w[i], 0x4140);
-      r[2 * i + 1] = int8x2_to_bf16x2(w[i], 0x4342);
-    }
+    for (int i = 0; i < 4; ++i) i8x4_to_f16(w[i], r[2 * i], r[2 * i + 1]);
   } else {
-    // INT4: nibble n of a word is element n.  (c ^ 8) in 0..15 is c + 8; 0x4300 | (c + 8) is 136 + c.
-#pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      uint32_t e[4];  // e[k]: elements k (low lane) and k + 4 (high lane)
-#pragma unroll
-      for (int k = 0; k < 4; ++k)
-        e[k] = bf16x2_sub(((w[i] >> (4 * k)) & 0x000f000fu) ^ 0x43084308u, 0x43084308u);
-      r[4 * i + 0] = __byte_perm(e[0], e[1], 0x5410);
-      r[4 * i + 1] = __byte_perm(e[2], e[3], 0x5410);
-      r[4 * i + 2] = __byte_perm(e[0], e[1], 0x7632);
-      r[4 * i + 3] = __byte_perm(e[2], e[3], 0x7632);
-    }
+    i4x8_to_f16_paired(w[0], r);
+    i4x8_to_f16_paired(w[1], r + 4);
   }
   lo = make_uint4(r[0], r[1], r[2], r[3]);
   hi = make_uint4(r[4], r[5], r[6], r[7]);
 }
 
-// Non-finite bf16 elements of a packed pair set to zero; true if there was one.
-__device__ __forceinline__ bool bf16x2_drop_nonfinite(uint32_t& w) {
+// Where element d of a group of eight stands in the paired order (0, 4, 1, 5, 2, 6, 3, 7).
+template <int KIND>
+__host__ __device__ constexpr int tree_place(int d) {
+  return KIND == TREE_INT4 ? (d & ~7) | ((d & 3) << 1) | ((d >> 2) & 1) : d;
+}
+
+// Non-finite elements of a packed pair (exponent field EXP all ones) set to zero; true if there was one.
+template <uint32_t EXP>
+__device__ __forceinline__ bool drop_nonfinite(uint32_t& w) {
   bool bad = false;
-  if ((w & 0x7f80u) == 0x7f80u) {
+  if ((w & EXP) == EXP) {
     w &= 0xffff0000u;
     bad = true;
   }
-  if ((w & 0x7f800000u) == 0x7f800000u) {
+  if ((w & (EXP << 16)) == (EXP << 16)) {
     w &= 0x0000ffffu;
     bad = true;
   }
@@ -293,7 +277,7 @@ __device__ __forceinline__ bool bf16x2_drop_nonfinite(uint32_t& w) {
 }
 
 // Row r of an MMA-ready V tile: zeros when drop, else its non-finite elements set to zero (true if any).
-template <int NBOX>
+template <int NBOX, uint32_t EXP>
 __device__ __forceinline__ bool tree_scrub_row(uint8_t* tile, int r, bool drop) {
   bool odd = false;
 #pragma unroll 1
@@ -303,10 +287,10 @@ __device__ __forceinline__ bool tree_scrub_row(uint8_t* tile, int r, bool drop) 
     bool bad = drop;
     if (!drop) {
       v4 = *q4;
-      bad |= bf16x2_drop_nonfinite(v4.x);
-      bad |= bf16x2_drop_nonfinite(v4.y);
-      bad |= bf16x2_drop_nonfinite(v4.z);
-      bad |= bf16x2_drop_nonfinite(v4.w);
+      bad |= drop_nonfinite<EXP>(v4.x);
+      bad |= drop_nonfinite<EXP>(v4.y);
+      bad |= drop_nonfinite<EXP>(v4.z);
+      bad |= drop_nonfinite<EXP>(v4.w);
       odd |= bad;
     }
     if (bad) *q4 = v4;
@@ -350,9 +334,9 @@ __device__ __forceinline__ unsigned long long tree_low_bits(int n) {
   return n >= 64 ? ~0ull : (1ull << n) - 1ull;
 }
 
-// Columns of the tile at kv0 that a row sees, 32 of them as a word: slots below base, and drafts in m.
-__device__ __forceinline__ uint32_t tree_seen_word(int w, int kv0, int base, unsigned long long m) {
-  const int pre = base - kv0 - 32 * w;  // leading columns of this word that are below base
+// Columns col .. col + 31 of the tile at kv0 that a row sees: slots below base, and drafts in m.
+__device__ __forceinline__ uint32_t tree_seen_word(int col, int kv0, int base, unsigned long long m) {
+  const int pre = base - kv0 - col;  // leading columns of this word that are below base
   uint32_t x = pre <= 0 ? 0u : (pre >= 32 ? ~0u : (1u << pre) - 1u);
   const int q = -pre;  // the draft that column 0 of the word would be
   if (q > -32 && q < 64) x |= q < 0 ? (uint32_t)(m << -q) : (uint32_t)(m >> q);
@@ -372,7 +356,8 @@ __global__ void __launch_bounds__((TreeCfg<KIND, D, PAIR>::THREADS), 1)
   // raw_* once per raw unit, sc_* once per tile, s_full / p_full once per tile of their slot.
   uint64_t* q_full = bars;
   uint64_t* q_empty = bars + 1;
-  uint64_t* u_full = bars + 2;
+  uint64_t* q_raw = bars + 2;  // coded caches: bf16 queries landed (q_full: they are f16)
+  uint64_t* u_full = bars + 3;
   uint64_t* u_empty = u_full + C::NU;
   uint64_t* raw_full = u_empty + C::NU;
   uint64_t* raw_empty = raw_full + C::NR;
@@ -390,13 +375,15 @@ __global__ void __launch_bounds__((TreeCfg<KIND, D, PAIR>::THREADS), 1)
   // odd_piece[i & 7] = i + 1 when piece i holds a non-finite draft V.  Whoever finds one runs at most a
   // ring of units ahead of the epilogue that asks (NU <= 6, two units or more a piece): eight entries.
   int* odd_piece = walk0 + 3;
+  uint32_t* q_max = reinterpret_cast<uint32_t*>(odd_piece + 8);  // [4] largest |q| (bf16 bits) per converter warp
 
   const int warp = threadIdx.x >> 5;
   const int lane = threadIdx.x & 31;
   const int rb = (int)blockIdx.x % p.n_rb;
 
   if (threadIdx.x == 0) {
-    mbar_init(q_full, 1);
+    mbar_init(q_full, CODED ? 4 : 1);
+    mbar_init(q_raw, 1);
     mbar_init(q_empty, 1);
     for (int i = 0; i < C::NU; ++i) {
       mbar_init(&u_full[i], CODED ? 4 : 1);  // converter warps, or the producer's expect_tx
@@ -468,11 +455,12 @@ __global__ void __launch_bounds__((TreeCfg<KIND, D, PAIR>::THREADS), 1)
       w.init(p, walk0);
       while (ok && w.next(p, it)) {
         if (qi > 0 && !(ok = mbar_wait<true>(q_empty, (qi - 1) & 1, SITE_TR_LOAD))) break;
-        mbar_arrive_expect_tx(q_full, C::NQ * C::NBOX * q_box);
+        uint64_t* q_land = CODED ? q_raw : q_full;
+        mbar_arrive_expect_tx(q_land, C::NQ * C::NBOX * q_box);
         q_pending = true;
         for (int s = 0; s < C::NQ; ++s)
           for (int bx = 0; bx < C::NBOX; ++bx)
-            tma_load_5d(smem + C::OFF_Q + s * C::TILE_BYTES + bx * C::BOX_BYTES, &tmQ, q_full, bx * 64, 0,
+            tma_load_5d(smem + C::OFF_Q + s * C::TILE_BYTES + bx * C::BOX_BYTES, &tmQ, q_land, bx * 64, 0,
                         (rb * C::NQ + s) * p.tps, it.kvh, it.b);
         if constexpr (PAIR) {
           for (int j = 0; j < it.n && ok; ++j) ok = load(&tmK, it, j) && load(&tmV, it, j);
@@ -486,7 +474,7 @@ __global__ void __launch_bounds__((TreeCfg<KIND, D, PAIR>::THREADS), 1)
       }
       if (!ok) {
         // Let every copy already issued land before the CTA's shared memory is released.
-        if (q_pending) mbar_wait_drain<true>(q_full, qi & 1, SITE_TR_DRAIN);
+        if (q_pending) mbar_wait_drain<true>(CODED ? q_raw : q_full, qi & 1, SITE_TR_DRAIN);
         constexpr int N = CODED ? C::NR : C::NU;
         uint64_t* full = CODED ? raw_full : u_full;
         for (int t = (u > N ? u - N : 0); t < u; ++t) mbar_wait_drain<true>(&full[t % N], (t / N) & 1, SITE_TR_DRAIN);
@@ -497,8 +485,8 @@ __global__ void __launch_bounds__((TreeCfg<KIND, D, PAIR>::THREADS), 1)
     // ------------------------------------------------------------------ MMA issuer
     if constexpr (!CODED) regs_dec<C::REGS_CTRL>();
     {
-      constexpr uint32_t idesc_qk = make_idesc_f16(128, 128, false, false, true);
-      constexpr uint32_t idesc_pv = make_idesc_f16(128, D, false, true, true);
+      constexpr uint32_t idesc_qk = make_idesc_f16(128, 128, false, false, !CODED);
+      constexpr uint32_t idesc_pv = make_idesc_f16(128, D, false, true, !CODED);
       constexpr uint32_t HI = sdesc_sw128_hi(1024);
       const uint32_t q_lo = sdesc_sw128_lo(smem_u32(smem + C::OFF_Q), 16);
       const uint32_t k_lo = sdesc_sw128_lo(smem_u32(smem + C::OFF_U), 16);
@@ -668,7 +656,7 @@ __global__ void __launch_bounds__((TreeCfg<KIND, D, PAIR>::THREADS), 1)
           __syncwarp();
           if (d >= 0) {
             const bool drop = d >= it.qn || !((any >> d) & 1);
-            if (tree_scrub_row<C::NBOX>(dst, t, drop)) odd_piece[qi & 7] = qi + 1;
+            if (tree_scrub_row<C::NBOX, C::EXP_MASK>(dst, t, drop)) odd_piece[qi & 7] = qi + 1;
           }
         }
         fence_proxy_async_smem();
@@ -682,6 +670,56 @@ __global__ void __launch_bounds__((TreeCfg<KIND, D, PAIR>::THREADS), 1)
       };
       // Scales of a tile: thread t loads those of token t one tile ahead.
       float ks = 0.f, vs = 0.f;
+      float q_down = 1.f;  // what undoes the queries' power of two
+      // The piece's queries, bf16 -> f16 in place, times a power of two that takes the largest |q| to
+      // [2^14, 2^15).  What falls below f16's normal range is then off by at most 2^-39 of the largest,
+      // far less than fp32 accumulation loses on it.
+      auto convert_q = [&]() -> bool {
+        if (!mbar_wait_warp<true>(q_raw, qi & 1, SITE_TR_CONV)) return false;
+        constexpr int CHUNKS = C::NQ * C::TILE_BYTES / 16;
+        uint4* qs = reinterpret_cast<uint4*>(smem + C::OFF_Q);
+        const int rows = p.tps * p.G;  // the others are never written: what they hold is not looked at
+        uint32_t top = 0;
+        for (int i = t; i < CHUNKS; i += 128) {
+          if (((i >> 3) & 127) >= rows) continue;
+          const uint4 x = qs[i];
+          const uint32_t w[4] = {x.x, x.y, x.z, x.w};
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            const uint32_t lo = w[k] & 0x7fffu, hi = (w[k] >> 16) & 0x7fffu;
+            if (lo < 0x7f80u) top = max(top, lo);
+            if (hi < 0x7f80u) top = max(top, hi);
+          }
+        }
+        top = __reduce_max_sync(0xffffffffu, top);
+        if (lane == 0) q_max[cw] = top;
+        named_barrier_sync(1, 128);
+        top = max(max(q_max[0], q_max[1]), max(q_max[2], q_max[3]));
+        const int shift = min(14 + 127 - max((int)(top >> 7), 1), 127);
+        const float up = __uint_as_float((uint32_t)(127 + shift) << 23);
+        q_down = exp2f((float)-shift);
+        for (int i = t; i < CHUNKS; i += 128) {
+          if (((i >> 3) & 127) >= rows) continue;
+          const uint4 x = qs[i];
+          const uint32_t w[4] = {x.x, x.y, x.z, x.w};
+          float f[8];
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            f[2 * k] = __uint_as_float(w[k] << 16) * up;
+            f[2 * k + 1] = __uint_as_float(w[k] & 0xffff0000u) * up;
+          }
+          if constexpr (KIND == TREE_INT4)
+            qs[i] = make_uint4(pack_f16x2(f[0], f[4]), pack_f16x2(f[1], f[5]), pack_f16x2(f[2], f[6]),
+                               pack_f16x2(f[3], f[7]));
+          else
+            qs[i] = make_uint4(pack_f16x2(f[0], f[1]), pack_f16x2(f[2], f[3]), pack_f16x2(f[4], f[5]),
+                               pack_f16x2(f[6], f[7]));
+        }
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(q_full);
+        return true;
+      };
       auto fetch = [&](const TreePiece& it, int j) {
         const int tok = (it.t0 + j) * 128 + t;
         ks = vs = 0.f;
@@ -697,15 +735,16 @@ __global__ void __launch_bounds__((TreeCfg<KIND, D, PAIR>::THREADS), 1)
       auto scales = [&](const TreePiece& it, int j, bool prefetch) -> bool {
         const int ss = g % C::NS;
         if (!mbar_wait_warp<true>(&sc_empty[ss], ((g / C::NS) & 1) ^ 1, SITE_TR_CONV)) return false;
-        float* dst = reinterpret_cast<float*>(smem + C::OFF_SC) + ss * 256;
+        float* dst = reinterpret_cast<float*>(smem + C::OFF_SC + ss * C::SC_BYTES);
         const int tok = (it.t0 + j) * 128 + t;
         // A draft's scale may be anything; the rows that do not see it must not meet it.
         if (tok >= it.len - it.qn && !(fabsf(vs) <= 3.4028234663852886e38f)) {
           vs = 0.f;
           if (tok < it.len) odd_piece[qi & 7] = qi + 1;
         }
-        dst[t] = ks * p.scale_log2;
+        dst[t] = ks * p.scale_log2 * q_down;
         dst[128 + t] = vs;
+        dst[256 + t] = fminf(fmaxf(__log2f(fabsf(vs)), -100.f), 100.f);
         if (prefetch) fetch(it, j + 1);
         __syncwarp();
         if (lane == 0) mbar_arrive(&sc_full[ss]);
@@ -718,6 +757,7 @@ __global__ void __launch_bounds__((TreeCfg<KIND, D, PAIR>::THREADS), 1)
       while (ok && w.next(p, it)) {
         const int n = it.n;
         fetch(it, 0);
+        ok = convert_q();
         for (int x = 0; x < 2 * n && ok; ++x) {  // the units of the piece, in the order of tree_v_unit
           bool is_v;
           int j;
@@ -748,11 +788,26 @@ __global__ void __launch_bounds__((TreeCfg<KIND, D, PAIR>::THREADS), 1)
     const bool row_used = r < p.tps * p.G && tok_i < p.n_q;
     int cs = 0, g = 0, qi = 0, ub = 0;  // tiles of this slot, tiles of the CTA, pieces, units before this piece
     bool ok = true;
-    TreeWalk w;
-    TreePiece it;
-    w.init(p, walk0);
-    while (ok && w.next(p, it)) {
-      const int n = it.n, base = it.len - it.qn;
+    // The walk and its piece are kept in shared memory, a copy per warp: between pieces they are dead weight,
+    // and the registers they took were spilled scores.
+    TreeWalk& sw = reinterpret_cast<TreeWalk*>(smem + C::OFF_WALK)[warp - 4];
+    TreePiece& it = reinterpret_cast<TreePiece*>(smem + C::OFF_WALK + 8 * sizeof(TreeWalk))[warp - 4];
+    auto next_piece = [&](bool first) -> bool {
+      TreeWalk w;
+      if (first) w.init(p, walk0);
+      else w = sw;
+      TreePiece x;
+      const bool more = w.next(p, x);
+      __syncwarp();  // every lane has read the old walk and piece
+      if (lane == 0 && more) {
+        sw = w;
+        it = x;
+      }
+      __syncwarp();
+      return more;
+    };
+    while (ok && next_piece(qi == 0)) {
+      const int n = it.n, t0 = it.t0, base = it.len - it.qn;
       const bool row_ok = row_used && tok_i < it.qn;
       unsigned long long m64 = 0;
       if (row_ok) m64 = (unsigned long long)__ldg(p.mask + (long long)it.b * p.n_q + tok_i) & tree_low_bits(it.qn);
@@ -761,50 +816,58 @@ __global__ void __launch_bounds__((TreeCfg<KIND, D, PAIR>::THREADS), 1)
         // tcgen05.ld/st are warp-collective: every lane takes the same branch around them.
         if (!(ok = mbar_wait_warp<true>(&s_full[slot], cs & 1, SITE_TR_SM_S))) break;
         tc_fence_after();
-        const int kv0 = (it.t0 + j) * 128;
+        const int kv0 = (t0 + j) * 128;
         const bool edge = kv0 + 128 > base;
-        // bf16: sr holds the row's 128 scores; coded caches: two chunks of 32, chunk c in sr + 32 (c & 1).
-        uint32_t sr[CODED ? 64 : 128];
-        auto chunk = [&](int c) -> uint32_t(&)[32] { return *reinterpret_cast<uint32_t(*)[32]>(&sr[(CODED ? c & 1 : c) * 32]); };
-        auto mask_chunk = [&](int c, uint32_t(&x)[32]) {
-          const uint32_t see = tree_seen_word(c, kv0, base, m64);
+        // bf16: sr holds the row's 128 scores, read as four chunks of 32; coded caches: two chunks of 16, chunk
+        // c in sr + 16 (c & 1).
+        constexpr int CH = CODED ? 16 : 32;
+        uint32_t sr[CODED ? 32 : 128];
+        auto chunk = [&](int c) -> uint32_t(&)[CH] {
+          return *reinterpret_cast<uint32_t(*)[CH]>(&sr[(CODED ? c & 1 : c) * CH]);
+        };
+        auto mask_chunk = [&](int c, uint32_t(&x)[CH]) {
+          const uint32_t see = tree_seen_word(c * CH, kv0, base, m64);
 #pragma unroll
-          for (int i = 0; i < 32; ++i)
+          for (int i = 0; i < CH; ++i)
             if (!((see >> i) & 1u)) x[i] = __float_as_uint(-INFINITY);
         };
-        const float* sc = nullptr;
+        uint32_t sc = 0;  // shared address of the tile's scales
         float mx0 = -INFINITY, mx1 = -INFINITY, mx2 = -INFINITY, mx3 = -INFINITY;
         if constexpr (CODED) {
           const int ss = (g + j) % C::NS;
           if (!(ok = mbar_wait_warp<true>(&sc_full[ss], ((g + j) / C::NS) & 1, SITE_TR_SM_SC))) break;
-          tmem_ld32(tS, chunk(0));
-          sc = reinterpret_cast<const float*>(smem + C::OFF_SC) + ss * 256;
+          tmem_ld16(tS, chunk(0));
+          sc = smem_u32(smem + C::OFF_SC) + ss * C::SC_BYTES;
+          auto find_max = [&](auto masked) {
 #pragma unroll 2
-          for (int c = 0; c < 4; ++c) {
-            uint32_t(&x)[32] = chunk(c);
-            tmem_wait_ld_regs(x);
-            tmem_ld32(tS + ((c + 1) & 3) * 32, chunk(c + 1));  // after the last, chunk 0 again for the weights
+            for (int c = 0; c < 8; ++c) {
+              uint32_t(&x)[CH] = chunk(c);
+              tmem_wait_ld_regs(x);
+              tmem_ld16(tS + ((c + 1) & 7) * CH, chunk(c + 1));  // after the last, chunk 0 again for the weights
 #pragma unroll
-            for (int i = 0; i < 32; i += 4) {
-              const float4 k4 = *reinterpret_cast<const float4*>(sc + c * 32 + i);
-              const float2 a = mul2(make_float2(__uint_as_float(x[i]), __uint_as_float(x[i + 1])),
-                                    make_float2(k4.x, k4.y));
-              const float2 b2 = mul2(make_float2(__uint_as_float(x[i + 2]), __uint_as_float(x[i + 3])),
-                                     make_float2(k4.z, k4.w));
-              x[i] = __float_as_uint(a.x);
-              x[i + 1] = __float_as_uint(a.y);
-              x[i + 2] = __float_as_uint(b2.x);
-              x[i + 3] = __float_as_uint(b2.y);
-            }
-            if (edge) mask_chunk(c, x);
+              for (int i = 0; i < CH; i += 4) {
+                const float4 k4 = lds_f4(sc + (c * CH + i) * 4), g4 = lds_f4(sc + 1024 + (c * CH + i) * 4);
+                const float2 a = fma2(make_float2(__uint_as_float(x[i]), __uint_as_float(x[i + 1])),
+                                      make_float2(k4.x, k4.y), make_float2(g4.x, g4.y));
+                const float2 b2 = fma2(make_float2(__uint_as_float(x[i + 2]), __uint_as_float(x[i + 3])),
+                                       make_float2(k4.z, k4.w), make_float2(g4.z, g4.w));
+                x[i] = __float_as_uint(a.x);
+                x[i + 1] = __float_as_uint(a.y);
+                x[i + 2] = __float_as_uint(b2.x);
+                x[i + 3] = __float_as_uint(b2.y);
+              }
+              if (masked.value) mask_chunk(c, x);
 #pragma unroll
-            for (int i = 0; i < 32; i += 8) {
-              mx0 = max3(mx0, __uint_as_float(x[i]), __uint_as_float(x[i + 1]));
-              mx1 = max3(mx1, __uint_as_float(x[i + 2]), __uint_as_float(x[i + 3]));
-              mx2 = max3(mx2, __uint_as_float(x[i + 4]), __uint_as_float(x[i + 5]));
-              mx3 = max3(mx3, __uint_as_float(x[i + 6]), __uint_as_float(x[i + 7]));
+              for (int i = 0; i < CH; i += 8) {
+                mx0 = max3(mx0, __uint_as_float(x[i]), __uint_as_float(x[i + 1]));
+                mx1 = max3(mx1, __uint_as_float(x[i + 2]), __uint_as_float(x[i + 3]));
+                mx2 = max3(mx2, __uint_as_float(x[i + 4]), __uint_as_float(x[i + 5]));
+                mx3 = max3(mx3, __uint_as_float(x[i + 6]), __uint_as_float(x[i + 7]));
+              }
             }
-          }
+          };
+          if (edge) find_max(std::true_type{});
+          else find_max(std::false_type{});
         } else {
 #pragma unroll
           for (int c = 0; c < 4; ++c) tmem_ld32(tS + c * 32, chunk(c));
@@ -853,41 +916,67 @@ __global__ void __launch_bounds__((TreeCfg<KIND, D, PAIR>::THREADS), 1)
           float2& a = (i & 3) == 0 ? a0 : (i & 3) == 1 ? a1 : (i & 3) == 2 ? a2 : a3;
           a = add2(a, e);
         };
-#pragma unroll(CODED ? 2 : 4)
-        for (int c = 0; c < 4; ++c) {
-          uint32_t pk[16];
-          uint32_t(&x)[32] = chunk(c);
-          if constexpr (CODED) {
-            tmem_wait_ld_regs(x);
-            // P lands in columns 16 c .. 16 c + 15, all below the chunk that is still to be read.
-            if (c < 3) tmem_ld32(tS + (c + 1) * 32, chunk(c + 1));
-          }
-          uint32_t see = ~0u;
-          if (CODED && edge) see = tree_seen_word(c, kv0, base, m64);
+        if constexpr (CODED) {
+          // A masked tile has a copy of its own: selects in the common one cost 1500 cycles a tile.
+          auto weights = [&](auto masked) {
+#pragma unroll 2
+            for (int c = 0; c < 8; ++c) {
+              uint32_t(&x)[CH] = chunk(c);
+              tmem_wait_ld_regs(x);
+              // P lands in columns 8 c .. 8 c + 7, all below the chunk that is still to be read.
+              if (c < 7) tmem_ld16(tS + (c + 1) * CH, chunk(c + 1));
 #pragma unroll
-          for (int i = 0; i < 16; ++i) {
-            const int k = c * 32 + 2 * i;
-            float2 y = make_float2(__uint_as_float(x[2 * i]), __uint_as_float(x[2 * i + 1]));
-            y = fma2(y, CODED ? *reinterpret_cast<const float2*>(sc + k) : c2, nm2);
-            float2 e;
-            e.x = ex2_approx(y.x);
-            e.y = ex2_approx(y.y);
-            if (CODED && edge) {
-              if (!((see >> (2 * i)) & 1u)) e.x = 0.f;
-              if (!((see >> (2 * i + 1)) & 1u)) e.y = 0.f;
+              for (int i = 0; i < CH; i += 4) {
+                const float4 k4 = lds_f4(sc + (c * CH + i) * 4);
+                const float2 a = fma2(make_float2(__uint_as_float(x[i]), __uint_as_float(x[i + 1])),
+                                      make_float2(k4.x, k4.y), nm2);
+                const float2 b2 = fma2(make_float2(__uint_as_float(x[i + 2]), __uint_as_float(x[i + 3])),
+                                       make_float2(k4.z, k4.w), nm2);
+                x[i] = __float_as_uint(a.x);
+                x[i + 1] = __float_as_uint(a.y);
+                x[i + 2] = __float_as_uint(b2.x);
+                x[i + 3] = __float_as_uint(b2.y);
+              }
+              if (masked.value) mask_chunk(c, x);
+              uint32_t pk[8];
+#pragma unroll
+              for (int i = 0; i < 8; i += 2) {
+                float2 e0 =
+                    make_float2(ex2_approx(__uint_as_float(x[2 * i])), ex2_approx(__uint_as_float(x[2 * i + 1])));
+                float2 e1 =
+                    make_float2(ex2_approx(__uint_as_float(x[2 * i + 2])), ex2_approx(__uint_as_float(x[2 * i + 3])));
+                add_sum(i, e0);
+                add_sum(i + 1, e1);
+                // The weight times its V scale is rounded once, to f16 (at most 2^-11 of it, or 2^-25 of the row's
+                // largest such product).
+                const float4 v4 = lds_f4(sc + 512 + (c * CH + 2 * i) * 4);
+                e0 = mul2(e0, make_float2(v4.x, v4.y));
+                e1 = mul2(e1, make_float2(v4.z, v4.w));
+                pk[i] = pack_f16x2(e0.x, e0.y);
+                pk[i + 1] = pack_f16x2(e1.x, e1.y);
+              }
+              tmem_st8(tS + c * 8, pk);
             }
-            // One rounding of the weight to bf16 (at most 2^-8 of it, and the errors of different
-            // keys are independent), of its product with the V scale for a coded cache.
-            if constexpr (CODED) {
-              add_sum(i, e);
-              e = mul2(e, *reinterpret_cast<const float2*>(sc + 128 + k));
-            } else {
+          };
+          if (edge) weights(std::true_type{});
+          else weights(std::false_type{});
+        } else {
+#pragma unroll
+          for (int c = 0; c < 4; ++c) {
+            uint32_t pk[16];
+            uint32_t(&x)[CH] = chunk(c);
+#pragma unroll
+            for (int i = 0; i < 16; ++i) {
+              const float2 y = fma2(make_float2(__uint_as_float(x[2 * i]), __uint_as_float(x[2 * i + 1])), c2, nm2);
+              const float2 e = make_float2(ex2_approx(y.x), ex2_approx(y.y));
               x[2 * i] = __float_as_uint(e.x);
               x[2 * i + 1] = __float_as_uint(e.y);
+              // One rounding of the weight to bf16 (at most 2^-8 of it, and the errors of different
+              // keys are independent).
+              pk[i] = pack_bf16x2(e.x, e.y);
             }
-            pk[i] = pack_bf16x2(e.x, e.y);
+            tmem_st16(tS + c * 16, pk);
           }
-          tmem_st16(tS + c * 16, pk);
         }
         tmem_wait_st();
         if constexpr (!CODED) {
@@ -900,7 +989,7 @@ __global__ void __launch_bounds__((TreeCfg<KIND, D, PAIR>::THREADS), 1)
             const int d = kv0 + r - base;
             if (d >= 0) {
               const bool drop = d >= it.qn || !((any >> d) & 1);
-              if (tree_scrub_row<C::NBOX>(smem + C::OFF_U + st * C::TILE_BYTES, r, drop)) odd_piece[qi & 7] = qi + 1;
+              if (tree_scrub_row<C::NBOX, C::EXP_MASK>(smem + C::OFF_U + st * C::TILE_BYTES, r, drop)) odd_piece[qi & 7] = qi + 1;
             }
             fence_proxy_async_smem();
           }
@@ -975,6 +1064,9 @@ __global__ void __launch_bounds__((TreeCfg<KIND, D, PAIR>::THREADS), 1)
           if (lane == 0) mbar_arrive(o_empty);
         }
         if (row_ok) {
+          float out[32];
+#pragma unroll
+          for (int i = 0; i < 32; ++i) out[i] = __uint_as_float(ov[tree_place<KIND>(i)]);
           if (fix && lse2 != -INFINITY) {  // non-finite values of the drafts this row sees
 #pragma unroll 1
             for (int dq = 0; dq < it.qn; ++dq) {
@@ -986,7 +1078,7 @@ __global__ void __launch_bounds__((TreeCfg<KIND, D, PAIR>::THREADS), 1)
 #pragma unroll
               for (int i = 0; i < 32; ++i) {
                 const float v = tree_v_value<KIND, D>(p, row, c * 32 + i);
-                if (!(fabsf(v) <= 3.4028234663852886e38f)) ov[i] = __float_as_uint(__uint_as_float(ov[i]) + v);
+                if (!(fabsf(v) <= 3.4028234663852886e38f)) out[i] += v;
               }
             }
           }
@@ -995,18 +1087,17 @@ __global__ void __launch_bounds__((TreeCfg<KIND, D, PAIR>::THREADS), 1)
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
               uint4 x;
-              x.x = pack_bf16x2(__uint_as_float(ov[8 * i + 0]), __uint_as_float(ov[8 * i + 1]));
-              x.y = pack_bf16x2(__uint_as_float(ov[8 * i + 2]), __uint_as_float(ov[8 * i + 3]));
-              x.z = pack_bf16x2(__uint_as_float(ov[8 * i + 4]), __uint_as_float(ov[8 * i + 5]));
-              x.w = pack_bf16x2(__uint_as_float(ov[8 * i + 6]), __uint_as_float(ov[8 * i + 7]));
+              x.x = pack_bf16x2(out[8 * i + 0], out[8 * i + 1]);
+              x.y = pack_bf16x2(out[8 * i + 2], out[8 * i + 3]);
+              x.z = pack_bf16x2(out[8 * i + 4], out[8 * i + 5]);
+              x.w = pack_bf16x2(out[8 * i + 6], out[8 * i + 7]);
               dst[i] = x;
             }
           } else {
             float4* dst = reinterpret_cast<float4*>(p.part_o + prow * D + c * 32);
 #pragma unroll
             for (int i = 0; i < 8; ++i)
-              dst[i] = make_float4(__uint_as_float(ov[4 * i]), __uint_as_float(ov[4 * i + 1]),
-                                   __uint_as_float(ov[4 * i + 2]), __uint_as_float(ov[4 * i + 3]));
+              dst[i] = make_float4(out[4 * i], out[4 * i + 1], out[4 * i + 2], out[4 * i + 3]);
           }
         }
       }
