@@ -46,6 +46,7 @@ EXPORTS = [
     "attn_prefill", "attn_decode_workspace_bytes", "attn_decode_num_splits", "attn_decode_splitkv",
     "attn_decode_splitkv_noalloc", "attn_decode_paged", "attn_prefill_varlen", "attn_decode_multi", "attn_decode_multi_workspace_bytes",
     "attn_decode_tree_workspace_bytes", "attn_decode_tree", "attn_decode_tree_paged",
+    "attn_tree_accept", "attn_pages_copy", "attn_pages_fork_workspace_bytes", "attn_pages_fork", "attn_pages_compact",
     "attn_merge_lse", "attn_stream_plan", "attn_stream_task", "attn_chunked_stream", "attn_status_string",
     "attn_last_cuda_error", "attn_device_status", "attn_set_wait_limit_ns", "attn_debug_wait_probe",
     "attn_debug_inject", "attn_debug_exp2",
@@ -164,6 +165,17 @@ def lib() -> ctypes.CDLL:
     L.attn_decode_tree.restype = i
     L.attn_decode_tree_paged.argtypes = [vp, vp, vp, i, vp, vp, vp, i, i, i, vp, vp, vp, i, Dims, vp, vp, vp, sz, vp]
     L.attn_decode_tree_paged.restype = i
+    pool = [vp, vp, vp, vp, i, i, i, i, i]
+    L.attn_tree_accept.argtypes = [vp, vp, vp, vp, i, i, i, i, vp, i, i, i, vp, vp, i, vp, vp, vp, vp]
+    L.attn_tree_accept.restype = i
+    L.attn_pages_copy.argtypes = pool + [vp, vp, i, vp]
+    L.attn_pages_copy.restype = i
+    L.attn_pages_fork_workspace_bytes.argtypes = [i, i]
+    L.attn_pages_fork_workspace_bytes.restype = sz
+    L.attn_pages_fork.argtypes = pool + [vp, vp, i, i, vp, vp, vp, vp, i, vp, vp, vp, vp, vp, sz, vp]
+    L.attn_pages_fork.restype = i
+    L.attn_pages_compact.argtypes = pool + [vp, i, i, vp, vp, vp, vp, vp, vp]
+    L.attn_pages_compact.restype = i
     L.attn_merge_lse.argtypes = [vp, vp, i, ll, i, vp, i, vp, i, vp]
     L.attn_merge_lse.restype = i
     L.attn_stream_plan.argtypes = [Dims, ll, i, ll, sz, ctypes.POINTER(StreamPlan)]
@@ -477,6 +489,135 @@ def attn_decode_tree_paged(q, k_pool, v_pool, page_table, kv_lens, tree_mask, *,
     """attn_decode_tree over a paged cache: pools, scale pools and page_table as for attn_decode_paged."""
     return _decode_tree("attn_decode_tree_paged", q, k_pool, v_pool, kv_lens, tree_mask, q_lens, k_scale, v_scale,
                         scale, o, lse, ws, want_lse, stream, kv_dtype, page_table)
+
+
+def _cache(k, v, k_scale, v_scale):
+    """Cache buffers of the upkeep calls: [layers, pages, page_size, Hkv, row] or one layer without the
+    first dimension, with scales [..., Hkv] for coded caches.  Returns (layers, pages, page_size, Hkv,
+    bytes of a row)."""
+    if k.dim() not in (4, 5):
+        raise ValueError(f"k: expected [layers, pages, page_size, Hkv, row] or one layer of it, got {tuple(k.shape)}")
+    coded = k.dtype in _ONE_BYTE
+    if not coded and k.dtype != torch.bfloat16:
+        raise ValueError(f"k: expected a bf16 or one-byte code cache, got {k.dtype}")
+    if coded != (k_scale is not None) or coded != (v_scale is not None):
+        raise ValueError("k_scale, v_scale: expected for coded caches, and for them alone")
+    _expect("k", k, k.dtype, k.shape)
+    _expect("v", v, k.dtype, k.shape)
+    _expect("k_scale", k_scale, torch.float32, k.shape[:-1])
+    _expect("v_scale", v_scale, torch.float32, k.shape[:-1])
+    shape = k.shape if k.dim() == 5 else (1, *k.shape)
+    if 0 in shape:
+        raise ValueError(f"k: expected a cache without empty dimensions, got {tuple(k.shape)}")
+    return shape[0], shape[1], shape[2], shape[3], shape[4] * k.element_size()
+
+
+def _table(page_table):
+    if page_table.dim() != 2:
+        raise ValueError(f"page_table: expected int32 [B, max_pages], got shape {tuple(page_table.shape)}")
+    _expect("page_table", page_table, torch.int32, page_table.shape)
+    return page_table.shape
+
+
+def attn_tree_accept(k, v, kv_lens, path, n_accepted, *, n_q: int | None = None, q_lens=None, page_table=None,
+                     k_scale=None, v_scale=None, kv_lens_out=None, stream=None):
+    """Keep the accepted drafts of each sequence: path int32 [B, n_q] (its first n_accepted[b] entries, draft
+    numbers) names the drafts whose cache rows move, in place and in every layer, to the slots behind
+    kv_lens[b] - q_lens[b] (q_lens None: n_q, which defaults to path.shape[1]).  k/v [layers, B, Tmax, Hkv, row] or
+    pools [layers, num_pages, page_size, Hkv, row] with page_table [B, max_pages], or one layer without
+    the first dimension -> kv_lens_out int32 [B]."""
+    device = _one_device(k=k, v=v, kv_lens=kv_lens, path=path, n_accepted=n_accepted, q_lens=q_lens,
+                         page_table=page_table, k_scale=k_scale, v_scale=v_scale, kv_lens_out=kv_lens_out)
+    layers, pages, page_size, Hkv, row = _cache(k, v, k_scale, v_scale)
+    B = kv_lens.shape[0]
+    n_q = path.shape[-1] if n_q is None else int(n_q)
+    _expect("kv_lens", kv_lens, torch.int32, (B,))
+    _expect("path", path, torch.int32, (B, n_q))
+    _expect("n_accepted", n_accepted, torch.int32, (B,))
+    _expect("q_lens", q_lens, torch.int32, (B,))
+    _expect("kv_lens_out", kv_lens_out, torch.int32, (B,))
+    if page_table is None and pages != B:
+        raise ValueError(f"k/v: expected {B} sequences (the length of kv_lens), got {pages}")
+    if page_table is not None and _table(page_table)[0] != B:
+        raise ValueError(f"page_table: expected {B} rows, got {page_table.shape[0]}")
+    if kv_lens_out is not None and kv_lens_out.data_ptr() == kv_lens.data_ptr():
+        raise ValueError("kv_lens_out: expected memory of its own, got kv_lens")
+    with _on(device, stream) as st:
+        if kv_lens_out is None:
+            kv_lens_out = torch.empty_like(kv_lens)
+        rc = lib().attn_tree_accept(_ptr(k), _ptr(v), _ptr(k_scale), _ptr(v_scale), layers, B, Hkv, row,
+                                    _ptr(page_table), 0 if page_table is None else page_table.shape[1], page_size,
+                                    pages, _ptr(kv_lens), _ptr(q_lens), n_q, _ptr(path), _ptr(n_accepted),
+                                    _ptr(kv_lens_out), st)
+    _check(rc, "attn_tree_accept")
+    return kv_lens_out
+
+
+def attn_pages_copy(k, v, src, dst, *, k_scale=None, v_scale=None, stream=None):
+    """Copy pages src[i] -> dst[i] (int32 [n] on the device) of pools [layers, num_pages, page_size, Hkv, row]
+    (or one layer), with their scale pools, in place."""
+    device = _one_device(k=k, v=v, src=src, dst=dst, k_scale=k_scale, v_scale=v_scale)
+    layers, pages, page_size, Hkv, row = _cache(k, v, k_scale, v_scale)
+    n = src.numel()
+    _expect("src", src, torch.int32, (n,))
+    _expect("dst", dst, torch.int32, (n,))
+    with _on(device, stream) as st:
+        rc = lib().attn_pages_copy(_ptr(k), _ptr(v), _ptr(k_scale), _ptr(v_scale), layers, pages, page_size, Hkv, row,
+                                   _ptr(src), _ptr(dst), n, st)
+    _check(rc, "attn_pages_copy")
+
+
+def attn_pages_fork_workspace_bytes(n_children: int, num_pages: int) -> int:
+    return int(lib().attn_pages_fork_workspace_bytes(int(n_children), int(num_pages)))
+
+
+def attn_pages_fork(k, v, page_table, kv_lens, ref_counts, parents, *, keep_lens, new_lens, k_scale=None,
+                    v_scale=None, ws=None, stream=None):
+    """The next generation of sequences over a pool: child c continues parents[c] (-1: nobody), keeps its
+    first keep_lens[c] tokens and has pages for new_lens[c] (all int32 [n_children] on the device).  Whole
+    kept pages are shared, cut ones kept or copied, the rest taken from the free pages in rising order; pages
+    nobody holds any more become free.  page_table int32 [B, max_pages], kv_lens int32 [B], ref_counts int32
+    [num_pages] -> (page_table [n_children, max_pages], kv_lens [n_children], ref_counts [num_pages],
+    info int32 [2] = free pages left, status), all new tensors; a status other than 0 (too few pages: budget;
+    bad arguments: invalid) leaves the old generation standing."""
+    device = _one_device(k=k, v=v, page_table=page_table, kv_lens=kv_lens, ref_counts=ref_counts, parents=parents,
+                         keep_lens=keep_lens, new_lens=new_lens, k_scale=k_scale, v_scale=v_scale, ws=ws)
+    layers, pages, page_size, Hkv, row = _cache(k, v, k_scale, v_scale)
+    B, max_pages = _table(page_table)
+    n = parents.numel()
+    _expect("kv_lens", kv_lens, torch.int32, (B,))
+    _expect("ref_counts", ref_counts, torch.int32, (pages,))
+    _expect("parents", parents, torch.int32, (n,))
+    _expect("keep_lens", keep_lens, torch.int32, (n,))
+    _expect("new_lens", new_lens, torch.int32, (n,))
+    if ws is not None and not ws.is_contiguous():
+        raise ValueError("ws: expected a contiguous workspace")
+    with _on(device, stream) as st:
+        out = [torch.empty(s, dtype=torch.int32, device=device) for s in ((n, max_pages), (n,), (pages,), (2,))]
+        if ws is None:
+            ws = torch.empty(attn_pages_fork_workspace_bytes(n, pages), dtype=torch.uint8, device=device)
+        rc = lib().attn_pages_fork(_ptr(k), _ptr(v), _ptr(k_scale), _ptr(v_scale), layers, pages, page_size, Hkv, row,
+                                   _ptr(page_table), _ptr(kv_lens), B, max_pages, _ptr(ref_counts), _ptr(parents),
+                                   _ptr(keep_lens), _ptr(new_lens), n, *map(_ptr, out), _ptr(ws),
+                                   ws.numel() * ws.element_size(), st)
+    _check(rc, "attn_pages_fork")
+    return tuple(out)
+
+
+def attn_pages_compact(k, v, page_table, ref_counts, *, k_scale=None, v_scale=None, stream=None):
+    """Move the live pages (ref_counts > 0) of a pool to its lowest page numbers, in place -> (page_table,
+    ref_counts in the new numbers, page_map int32 [num_pages]: where each page went, -1 for free ones,
+    info int32 [2] = live pages, pages moved), all new tensors."""
+    device = _one_device(k=k, v=v, page_table=page_table, ref_counts=ref_counts, k_scale=k_scale, v_scale=v_scale)
+    layers, pages, page_size, Hkv, row = _cache(k, v, k_scale, v_scale)
+    B, max_pages = _table(page_table)
+    _expect("ref_counts", ref_counts, torch.int32, (pages,))
+    with _on(device, stream) as st:
+        out = [torch.empty(s, dtype=torch.int32, device=device) for s in ((B, max_pages), (pages,), (pages,), (2,))]
+        rc = lib().attn_pages_compact(_ptr(k), _ptr(v), _ptr(k_scale), _ptr(v_scale), layers, pages, page_size, Hkv,
+                                      row, _ptr(page_table), B, max_pages, _ptr(ref_counts), *map(_ptr, out), st)
+    _check(rc, "attn_pages_compact")
+    return tuple(out)
 
 
 NOALLOC_SCRATCH_BYTES = 4 << 20

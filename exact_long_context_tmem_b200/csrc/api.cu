@@ -17,6 +17,7 @@
 #include "decode_fp8.cuh"
 #include "decode_int.cuh"
 #include "merge.cuh"
+#include "pages.cuh"
 #include "prefill.cuh"
 #include "tree.cuh"
 
@@ -549,6 +550,43 @@ static attn_status_t tree_call(const void* q, const void* k, const void* v, attn
   return launch_tree<TREE_BF16, 128>(q, k, v, pg, d, t, p, stream);
 }
 
+// ---------------------------------------------------------------- cache upkeep
+
+// The buffers of a cache [layers, pages, page_size, Hkv, row_bytes] with its optional scales, checked.
+static attn_status_t cache_bufs(void* k, void* v, float* ks, float* vs, int n_layers, int num_pages, int page_size,
+                                int Hkv, int row_bytes, CacheBufs* c) {
+  if (n_layers < 0 || num_pages < 1 || page_size < 1 || Hkv < 1 || row_bytes < 16 || row_bytes % 16 != 0)
+    return ATTN_ERR_INVALID_ARG;
+  if (!k || !v || !aligned16(k) || !aligned16(v) || (ks != nullptr) != (vs != nullptr)) return ATTN_ERR_INVALID_ARG;
+  if (ks && (!aligned4(ks) || !aligned4(vs))) return ATTN_ERR_INVALID_ARG;
+  if ((long long)Hkv * row_bytes > (1 << 24)) return ATTN_ERR_UNSUPPORTED;
+  c->n = ks ? 4 : 2;
+  c->n_layers = n_layers;
+  c->page_size = page_size;
+  c->num_pages = num_pages;
+  void* ptr[4] = {k, v, ks, vs};
+  long long chunks = 0;
+  for (int i = 0; i < c->n; ++i) {
+    c->p[i] = static_cast<char*>(ptr[i]);
+    c->tok[i] = i < 2 ? Hkv * row_bytes : Hkv * 4;
+    c->vec[i] = c->tok[i] % 16 == 0 && aligned16(ptr[i]) ? 16 : 4;
+    const long long page = (long long)page_size * c->tok[i];
+    c->layer[i] = page * num_pages;
+    c->chunk0[i] = (int)chunks;
+    chunks += (page + kChunkBytes - 1) / kChunkBytes;
+    if (chunks > 0x3fffffff) return ATTN_ERR_UNSUPPORTED;
+  }
+  for (int i = c->n; i < 5; ++i) c->chunk0[i] = (int)chunks;
+  return ATTN_OK;
+}
+
+// CTAs for a number of 16 KB copy units: eight a processor keep HBM busy, fewer when there is less to do.
+static int copy_grid(long long units) {
+  int sms = 148, dev = 0;
+  if (cudaGetDevice(&dev) == cudaSuccess) cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
+  return (int)std::max(1LL, std::min<long long>(units, 8LL * std::max(sms, 1)));
+}
+
 // ---------------------------------------------------------------- diagnostics
 
 __global__ void exp2_probe_kernel(const float* x, float* y, long long n, int mode) {
@@ -856,6 +894,166 @@ attn_status_t attn_decode_tree_paged(const void* q, const void* k_pool, const vo
   const DecodePaging pg{page_table, max_pages, page_size, num_pages};
   return tree_call(q, k_pool, v_pool, kv_dtype, k_scale_pool, v_scale_pool, pg, kv_lens, q_lens, tree_mask,
                    max_pages * page_size, n_q, dims, o, lse, ws, ws_bytes, reinterpret_cast<cudaStream_t>(stream));
+}
+
+attn_status_t attn_tree_accept(void* k, void* v, float* k_scale, float* v_scale, int n_layers, int B, int Hkv,
+                               int row_bytes, const int* page_table, int max_pages, int page_size, int num_pages,
+                               const int* kv_lens, const int* q_lens, int n_q, const int* path, const int* n_accepted,
+                               int* kv_lens_out, void* stream) {
+  if (B < 0 || n_q < 0 || n_layers < 0 || (page_table && (max_pages < 1 || page_size < 128 || page_size % 128 != 0)))
+    return ATTN_ERR_INVALID_ARG;
+  if (B == 0) return ATTN_OK;
+  if (!kv_lens || !path || !n_accepted || !kv_lens_out || kv_lens_out == kv_lens) return ATTN_ERR_INVALID_ARG;
+  if (!aligned4(kv_lens) || !aligned4(path) || !aligned4(n_accepted) || !aligned4(kv_lens_out) ||
+      (q_lens && !aligned4(q_lens)) || (page_table && !aligned4(page_table)))
+    return ATTN_ERR_INVALID_ARG;
+  AcceptParams p{};
+  const attn_status_t st =
+      cache_bufs(k, v, k_scale, v_scale, n_layers, page_table ? num_pages : B, page_size, Hkv, row_bytes, &p.c);
+  if (st != ATTN_OK) return st;
+  if (n_q > 64 || B > 65535 || n_layers > 65535) return ATTN_ERR_UNSUPPORTED;
+  if (page_table && (long long)max_pages * page_size > 0x7fffffffLL) return ATTN_ERR_UNSUPPORTED;
+  if (n_layers == 0) return ATTN_ERR_INVALID_ARG;  // no block would write kv_lens_out
+  p.B = B;
+  p.n_q = n_q;
+  p.max_pages = max_pages;
+  p.page_table = page_table;
+  p.kv_lens = kv_lens;
+  p.q_lens = q_lens;
+  p.path = path;
+  p.n_acc = n_accepted;
+  p.kv_lens_out = kv_lens_out;
+  long long cols = 0;
+  for (int i = 0; i < p.c.n; ++i) cols += p.c.tok[i] / p.c.vec[i];
+  const dim3 grid((unsigned)((cols + 127) / 128), (unsigned)B, (unsigned)n_layers);
+  tree_accept_kernel<<<grid, 128, 0, reinterpret_cast<cudaStream_t>(stream)>>>(p);
+  ATTN_CUDA(cudaGetLastError());
+  return ATTN_OK;
+}
+
+attn_status_t attn_pages_copy(void* k, void* v, float* k_scale, float* v_scale, int n_layers, int num_pages,
+                              int page_size, int Hkv, int row_bytes, const int* src, const int* dst, int n,
+                              void* stream) {
+  if (n < 0) return ATTN_ERR_INVALID_ARG;
+  CopyParams p{};
+  const attn_status_t st = cache_bufs(k, v, k_scale, v_scale, n_layers, num_pages, page_size, Hkv, row_bytes, &p.c);
+  if (st != ATTN_OK) return st;
+  if (num_pages > kMaxPages) return ATTN_ERR_UNSUPPORTED;
+  if (n == 0 || n_layers == 0) return ATTN_OK;
+  if (!src || !dst || !aligned4(src) || !aligned4(dst)) return ATTN_ERR_INVALID_ARG;
+  p.src = src;
+  p.dst = dst;
+  p.n = n;
+  static std::atomic<uint64_t> smem_done{0};
+  const attn_status_t s2 = ensure_smem(pages_copy_kernel, kMaxPages / 8, smem_done);
+  if (s2 != ATTN_OK) return s2;
+  const int smem = (num_pages + 31) / 32 * 4;
+  pages_copy_kernel<<<copy_grid((long long)n * n_layers * p.c.chunk0[p.c.n]), kCopyThreads, smem,
+                      reinterpret_cast<cudaStream_t>(stream)>>>(p);
+  ATTN_CUDA(cudaGetLastError());
+  return ATTN_OK;
+}
+
+attn_status_t attn_pages_compact(void* k, void* v, float* k_scale, float* v_scale, int n_layers, int num_pages,
+                                 int page_size, int Hkv, int row_bytes, const int* page_table, int B, int max_pages,
+                                 const int* ref_counts, int* table_out, int* refs_out, int* page_map, int* info,
+                                 void* stream) {
+  if (B < 0 || max_pages < 0) return ATTN_ERR_INVALID_ARG;
+  CompactParams p{};
+  const attn_status_t st = cache_bufs(k, v, k_scale, v_scale, n_layers, num_pages, page_size, Hkv, row_bytes, &p.c);
+  if (st != ATTN_OK) return st;
+  p.n_entries = (long long)B * max_pages;
+  if (!ref_counts || !refs_out || !page_map || !info || (p.n_entries > 0 && (!page_table || !table_out)))
+    return ATTN_ERR_INVALID_ARG;
+  if (!aligned4(ref_counts) || !aligned4(refs_out) || !aligned4(page_map) || !aligned4(info) ||
+      !aligned4(page_table) || !aligned4(table_out) || refs_out == ref_counts ||
+      (p.n_entries > 0 && table_out == page_table))
+    return ATTN_ERR_INVALID_ARG;
+  if (num_pages > kMaxPages) return ATTN_ERR_UNSUPPORTED;
+  p.table = page_table;
+  p.refs = ref_counts;
+  p.table_out = table_out;
+  p.refs_out = refs_out;
+  p.page_map = page_map;
+  p.info = info;
+  static std::atomic<uint64_t> smem_done{0};
+  const attn_status_t s2 = ensure_smem(pages_compact_kernel, kMaxPages / 128 * 20, smem_done);
+  if (s2 != ATTN_OK) return s2;
+  const int smem = (num_pages + 127) / 128 * 20;
+  // At most half the pages move.
+  const long long units = std::max<long long>((long long)num_pages / 2 * n_layers * p.c.chunk0[p.c.n],
+                                              std::max<long long>(p.n_entries, num_pages) / kCopyThreads);
+  pages_compact_kernel<<<copy_grid(units), kCopyThreads, smem, reinterpret_cast<cudaStream_t>(stream)>>>(p);
+  ATTN_CUDA(cudaGetLastError());
+  return ATTN_OK;
+}
+
+// Counts and claims of the pages fit in shared memory up to this many pages.
+static constexpr int kForkSmemPages = 25600;
+
+size_t attn_pages_fork_workspace_bytes(int n_children, int num_pages) {
+  if (n_children < 0 || num_pages < 1) return 0;
+  const size_t pages = (size_t)num_pages * (num_pages > kForkSmemPages ? 3 : 1);
+  return ((size_t)n_children * 4 + pages + 4) * sizeof(int);
+}
+
+attn_status_t attn_pages_fork(void* k, void* v, float* k_scale, float* v_scale, int n_layers, int num_pages,
+                              int page_size, int Hkv, int row_bytes, const int* page_table, const int* kv_lens, int B,
+                              int max_pages, const int* ref_counts, const int* parents, const int* keep_lens,
+                              const int* new_lens, int n_children, int* table_out, int* lens_out, int* refs_out,
+                              int* info, void* ws, size_t ws_bytes, void* stream) {
+  if (B < 0 || n_children < 0 || max_pages < 1) return ATTN_ERR_INVALID_ARG;
+  ForkParams p{};
+  const attn_status_t st = cache_bufs(k, v, k_scale, v_scale, n_layers, num_pages, page_size, Hkv, row_bytes, &p.c);
+  if (st != ATTN_OK) return st;
+  if (!ref_counts || !refs_out || !info || !ws || (B > 0 && (!page_table || !kv_lens)) ||
+      (n_children > 0 && (!parents || !keep_lens || !new_lens || !table_out || !lens_out)))
+    return ATTN_ERR_INVALID_ARG;
+  const void* ptrs[] = {ref_counts, refs_out, info, ws, page_table, kv_lens, parents, keep_lens, new_lens, table_out,
+                        lens_out};
+  for (const void* x : ptrs)
+    if (!aligned4(x)) return ATTN_ERR_INVALID_ARG;
+  if (ws_bytes < attn_pages_fork_workspace_bytes(n_children, num_pages)) return ATTN_ERR_INVALID_ARG;
+  if (refs_out == ref_counts || (n_children > 0 && (table_out == page_table || lens_out == kv_lens)))
+    return ATTN_ERR_INVALID_ARG;
+  if ((long long)max_pages * page_size > 0x7fffffffLL || (long long)n_children * max_pages >= (1 << 30) ||
+      (long long)B * max_pages > 0x7fffffffLL)
+    return ATTN_ERR_UNSUPPORTED;
+  p.B = B;
+  p.n_child = n_children;
+  p.max_pages = max_pages;
+  p.table = page_table;
+  p.lens = kv_lens;
+  p.refs = ref_counts;
+  p.parents = parents;
+  p.keep = keep_lens;
+  p.new_lens = new_lens;
+  p.table_out = table_out;
+  p.lens_out = lens_out;
+  p.refs_out = refs_out;
+  p.info = info;
+  p.head = static_cast<int*>(ws);
+  p.child = p.head + 4;
+  p.copies = p.child + n_children;
+  p.fresh = p.copies + 3 * (size_t)n_children;
+  p.count = p.fresh + num_pages;
+  p.claim = p.count + num_pages;
+  cudaStream_t cs = reinterpret_cast<cudaStream_t>(stream);
+  if (num_pages <= kForkSmemPages) {
+    static std::atomic<uint64_t> smem_done{0};
+    const attn_status_t s2 = ensure_smem(pages_fork_plan_kernel<true>, kForkSmemPages * 8, smem_done);
+    if (s2 != ATTN_OK) return s2;
+    pages_fork_plan_kernel<true><<<1, kForkThreads, num_pages * 8, cs>>>(p);
+  } else {
+    pages_fork_plan_kernel<false><<<1, kForkThreads, 0, cs>>>(p);
+  }
+  ATTN_CUDA(cudaGetLastError());
+  if (n_children == 0) return ATTN_OK;
+  const long long units = std::max<long long>((long long)n_children * n_layers * p.c.chunk0[p.c.n],
+                                              ((long long)n_children * max_pages + kCopyThreads - 1) / kCopyThreads);
+  pages_fork_apply_kernel<<<copy_grid(units), kCopyThreads, 0, cs>>>(p);
+  ATTN_CUDA(cudaGetLastError());
+  return ATTN_OK;
 }
 
 // Split-KV decode without allocation: the split partials live in this static device array

@@ -1,0 +1,572 @@
+// Keeping a KV cache: the accepted path of a draft tree, and the pages of a paged cache (LLM-CoOpt
+// summary, "Opt-Pa": fixed-size pages, mapped on demand; ONNX Runtime packed-QSA analysis, "Code
+// analysis" 2: what follows the verification of several tokens).
+//
+// Nothing here is computed: rows and pages move as bytes, and small integer tables are rewritten on the
+// device, so a decoding step never waits for the host.  Cache buffers are K, V and, for coded caches, their
+// scales, each [layers, pages, page_size, tok_bytes].
+#pragma once
+
+#include "ptx.cuh"
+
+namespace attn {
+
+struct CacheBufs {
+  char* p[4];             // K, V, K scales, V scales
+  long long layer[4];     // bytes of a layer
+  int tok[4];             // bytes of a token
+  int vec[4];             // bytes a thread moves at a time: 16, or 4 (scales whose address or size asks for it)
+  int chunk0[5];          // first chunk of each buffer's page, and the chunks of all of them
+  int n, n_layers;
+  int page_size, num_pages;
+};
+
+static constexpr int kCopyThreads = 256;
+static constexpr int kChunkBytes = kCopyThreads * 4 * 16;  // what a CTA has in flight
+static constexpr int kMaxPages = 1 << 20;                  // bitmaps of pages live in shared memory
+
+// One chunk of the first n_tok tokens of a page, src -> dst, in one layer.
+__device__ __forceinline__ void copy_chunk(const CacheBufs& c, int src, int dst, int n_tok, int layer, int chunk) {
+  int s = 0;
+  while (chunk >= c.chunk0[s + 1]) ++s;
+  const long long page = (long long)c.page_size * c.tok[s];
+  const long long bytes = (long long)n_tok * c.tok[s];
+  const long long off = (long long)(chunk - c.chunk0[s]) * kChunkBytes;
+  const char* from = c.p[s] + layer * c.layer[s] + src * page;
+  char* to = c.p[s] + layer * c.layer[s] + dst * page;
+  const long long end = min(bytes, off + kChunkBytes);
+  if (c.vec[s] == 16) {
+    uint4 x[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const long long o = off + (threadIdx.x + i * kCopyThreads) * 16;
+      if (o < end) x[i] = *reinterpret_cast<const uint4*>(from + o);
+    }
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const long long o = off + (threadIdx.x + i * kCopyThreads) * 16;
+      if (o < end) *reinterpret_cast<uint4*>(to + o) = x[i];
+    }
+  } else {
+    for (long long o = off + threadIdx.x * 4; o < end; o += kCopyThreads * 4)
+      *reinterpret_cast<uint32_t*>(to + o) = *reinterpret_cast<const uint32_t*>(from + o);
+  }
+}
+
+// ------------------------------------------------------------------------------- accepted path
+
+struct AcceptParams {
+  CacheBufs c;
+  int B, n_q, max_pages;
+  const int* page_table;  // or null: sequence b is page b
+  const int* kv_lens;
+  const int* q_lens;      // or null: n_q
+  const int* path;        // [B, n_q]
+  const int* n_acc;       // [B]
+  int* kv_lens_out;
+};
+
+// Block (x, b, layer): columns of tokens, in order of the path.  A thread owns its columns of every moved
+// token, so nothing is read after another thread has overwritten it; on a rising path (p_j >= j) rows
+// are read in batches ahead of the writes, which only reach slots that later steps do not read.  Any
+// other path goes through registers whole, a word at a time.
+__global__ void __launch_bounds__(128) tree_accept_kernel(const AcceptParams p) {
+  const int b = blockIdx.y, layer = blockIdx.z;
+  __shared__ long long from[64], to[64];  // token rows (page * page_size + slot)
+  __shared__ int bad, falling;
+  const int qn = p.q_lens ? p.q_lens[b] : p.n_q;
+  const int len = p.kv_lens[b], acc = p.n_acc[b];
+  const int base = len - qn;
+  const int cap = p.page_table ? p.max_pages * p.c.page_size : p.c.page_size;
+  if (threadIdx.x == 0) {
+    bad = qn < 0 || qn > p.n_q || len < 0 || base < 0 || len > cap || acc < 0 || acc > qn;
+    falling = 0;
+  }
+  __syncthreads();
+  if (!bad && threadIdx.x < acc) {
+    const int j = threadIdx.x, x = p.path[(long long)b * p.n_q + j];
+    bool wrong = x < 0 || x >= qn;
+    if (!wrong && j > 0 && p.path[(long long)b * p.n_q + j - 1] >= x) falling = 1;
+    auto row = [&](int tok) -> long long {
+      int pg = b;
+      if (p.page_table) {
+        pg = p.page_table[(long long)b * p.max_pages + tok / p.c.page_size];
+        if (pg < 0 || pg >= p.c.num_pages) wrong = true;
+        tok %= p.c.page_size;
+      }
+      return (long long)pg * p.c.page_size + tok;
+    };
+    if (!wrong) {
+      to[j] = row(base + j);
+      from[j] = row(base + x);
+    }
+    if (wrong) bad = 1;
+  }
+  __syncthreads();
+  if (bad) {  // left as it was
+    if (threadIdx.x == 0 && blockIdx.x == 0 && layer == 0) {
+      p.kv_lens_out[b] = len;
+      record_arg_error(ATTN_DEV_BAD_INDEX, SITE_ACCEPT);
+    }
+    return;
+  }
+  if (threadIdx.x == 0 && blockIdx.x == 0 && layer == 0) p.kv_lens_out[b] = base + acc;
+  int col = blockIdx.x * 128 + threadIdx.x, s = 0;
+  for (; s < p.c.n; ++s) {
+    const int cols = p.c.tok[s] / p.c.vec[s];
+    if (col < cols) break;
+    col -= cols;
+  }
+  if (s == p.c.n) return;
+  const int tok = p.c.tok[s], vec = p.c.vec[s];
+  char* mem = p.c.p[s] + layer * p.c.layer[s] + col * vec;
+  if (falling) {
+    for (int w = 0; w < vec; w += 4) {
+      uint32_t x[64];
+#pragma unroll
+      for (int j = 0; j < 64; ++j)
+        if (j < acc) x[j] = *reinterpret_cast<const uint32_t*>(mem + from[j] * tok + w);
+#pragma unroll
+      for (int j = 0; j < 64; ++j)
+        if (j < acc) *reinterpret_cast<uint32_t*>(mem + to[j] * tok + w) = x[j];
+    }
+  } else if (vec == 16) {
+    for (int j0 = 0; j0 < acc; j0 += 8) {
+      uint4 x[8];
+#pragma unroll
+      for (int i = 0; i < 8; ++i)
+        if (j0 + i < acc && from[j0 + i] != to[j0 + i])
+          x[i] = *reinterpret_cast<const uint4*>(mem + from[j0 + i] * tok);
+#pragma unroll
+      for (int i = 0; i < 8; ++i)
+        if (j0 + i < acc && from[j0 + i] != to[j0 + i]) *reinterpret_cast<uint4*>(mem + to[j0 + i] * tok) = x[i];
+    }
+  } else {
+    for (int j = 0; j < acc; ++j)
+      if (from[j] != to[j])
+        *reinterpret_cast<uint32_t*>(mem + to[j] * tok) = *reinterpret_cast<const uint32_t*>(mem + from[j] * tok);
+  }
+}
+
+// ------------------------------------------------------------------------------- page copies
+
+struct CopyParams {
+  CacheBufs c;
+  const int* src;
+  const int* dst;
+  int n;
+};
+
+// Every CTA checks the whole list itself (a bitmap of destinations, n reads from L2), so that all of them
+// refuse a list whose pages are out of range, written twice, or both written and read.
+__global__ void __launch_bounds__(kCopyThreads) pages_copy_kernel(const CopyParams p) {
+  extern __shared__ uint32_t written[];
+  __shared__ int bad;
+  const int words = (p.c.num_pages + 31) / 32;
+  for (int i = threadIdx.x; i < words; i += kCopyThreads) written[i] = 0;
+  if (threadIdx.x == 0) bad = 0;
+  __syncthreads();
+  for (int i = threadIdx.x; i < p.n; i += kCopyThreads) {
+    const int a = p.src[i], d = p.dst[i];
+    if (a < 0 || a >= p.c.num_pages || d < 0 || d >= p.c.num_pages) bad = 1;
+    else if (a != d && (atomicOr(&written[d >> 5], 1u << (d & 31)) >> (d & 31)) & 1u) bad = 1;
+  }
+  __syncthreads();
+  if (!bad)
+    for (int i = threadIdx.x; i < p.n; i += kCopyThreads) {
+      const int a = p.src[i];
+      if (a != p.dst[i] && (written[a >> 5] >> (a & 31)) & 1u) bad = 1;
+    }
+  __syncthreads();
+  if (bad) {
+    if (threadIdx.x == 0 && blockIdx.x == 0) record_arg_error(ATTN_DEV_BAD_INDEX, SITE_PAGES_COPY);
+    return;
+  }
+  const int per = p.c.chunk0[p.c.n];
+  const long long units = (long long)p.n * p.c.n_layers * per;
+  for (long long u = blockIdx.x; u < units; u += gridDim.x) {
+    const int chunk = (int)(u % per);
+    const long long r = u / per;
+    const int i = (int)(r / p.c.n_layers), a = p.src[i], d = p.dst[i];
+    if (a != d) copy_chunk(p.c, a, d, p.c.page_size, (int)(r % p.c.n_layers), chunk);
+  }
+}
+
+// ------------------------------------------------------------------------------- compaction
+
+struct CompactParams {
+  CacheBufs c;
+  const int* table;
+  long long n_entries;  // B * max_pages
+  const int* refs;
+  int* table_out;
+  int* refs_out;
+  int* page_map;
+  int* info;  // live pages, moved pages
+};
+
+// Pages that are live, as a bitmap with the number of live pages before each group of 128.
+struct LivePages {
+  const uint4* bits;
+  const int* before;
+  int groups;
+  __device__ __forceinline__ static uint32_t word(const uint4& g, int i) {
+    return i == 0 ? g.x : i == 1 ? g.y : i == 2 ? g.z : g.w;
+  }
+  __device__ __forceinline__ bool live(int p) const { return (word(bits[p >> 7], (p >> 5) & 3) >> (p & 31)) & 1u; }
+  __device__ __forceinline__ int rank(int p) const {  // live pages below p
+    const uint4 g = bits[p >> 7];
+    int r = before[p >> 7];
+    const int w = (p >> 5) & 3;
+    if (w > 0) r += __popc(g.x);
+    if (w > 1) r += __popc(g.y);
+    if (w > 2) r += __popc(g.z);
+    return r + __popc(word(g, w) & ((1u << (p & 31)) - 1u));
+  }
+  // The k-th page (from 0) that is live (or, free), given that there is one.
+  __device__ __forceinline__ int select(int k, bool free_pages) const {
+    int lo = 0, hi = groups - 1;  // the last group with at most k such pages before it
+    while (lo < hi) {
+      const int mid = (lo + hi + 1) >> 1;
+      const int n = free_pages ? mid * 128 - before[mid] : before[mid];
+      if (n <= k) lo = mid;
+      else hi = mid - 1;
+    }
+    k -= free_pages ? lo * 128 - before[lo] : before[lo];
+    const uint4 g = bits[lo];
+    int p = lo * 128;
+#pragma unroll
+    for (int w = 0; w < 4; ++w) {
+      const uint32_t x = free_pages ? ~word(g, w) : word(g, w);
+      const int n = __popc(x);
+      if (k >= n) {
+        k -= n;
+        p += 32;
+        continue;
+      }
+      uint32_t y = x;
+      for (int i = 0; i < k; ++i) y &= y - 1;
+      return p + __ffs(y) - 1;
+    }
+    return p;
+  }
+};
+
+// Live pages at or past n_live move into the free ones below, both in rising order.  Every CTA builds the
+// bitmap and its prefix itself (4 bytes a page from L2): one launch, and no CTA waits for another.
+__global__ void __launch_bounds__(kCopyThreads) pages_compact_kernel(const CompactParams p) {
+  extern __shared__ uint4 bits[];
+  __shared__ int warp_sum[kCopyThreads / 32];
+  const int N = p.c.num_pages, groups = (N + 127) / 128;
+  int* before = reinterpret_cast<int*>(bits + groups);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  bool negative = false;
+  // A thread takes whole words: the loads are 16 bytes, eight in flight.
+  for (int w = threadIdx.x; w < groups * 4; w += kCopyThreads) {
+    uint32_t x = 0;
+    const int p0 = w * 32;
+    if (p0 + 32 <= N && (reinterpret_cast<uintptr_t>(p.refs) & 15) == 0) {
+      int4 r[8];
+#pragma unroll
+      for (int i = 0; i < 8; ++i) r[i] = reinterpret_cast<const int4*>(p.refs + p0)[i];
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        x |= (uint32_t)(r[i].x > 0) << (4 * i) | (uint32_t)(r[i].y > 0) << (4 * i + 1) |
+             (uint32_t)(r[i].z > 0) << (4 * i + 2) | (uint32_t)(r[i].w > 0) << (4 * i + 3);
+        negative |= (r[i].x | r[i].y | r[i].z | r[i].w) < 0;
+      }
+    } else {
+      for (int i = 0; i < 32 && p0 + i < N; ++i) {
+        const int r = p.refs[p0 + i];
+        x |= (uint32_t)(r > 0) << i;
+        negative |= r < 0;
+      }
+    }
+    reinterpret_cast<uint32_t*>(bits)[w] = x;
+  }
+  __syncthreads();
+  int total = 0;
+  for (int g0 = 0; g0 < groups; g0 += kCopyThreads) {
+    const int g = g0 + threadIdx.x;
+    int n = 0;
+    if (g < groups) {
+      const uint4 x = bits[g];
+      n = __popc(x.x) + __popc(x.y) + __popc(x.z) + __popc(x.w);
+    }
+    int incl = n;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int y = __shfl_up_sync(0xffffffffu, incl, o);
+      if (lane >= o) incl += y;
+    }
+    if (lane == 31) warp_sum[warp] = incl;
+    __syncthreads();
+    int prior = 0, all = 0;
+#pragma unroll
+    for (int i = 0; i < kCopyThreads / 32; ++i) {
+      if (i < warp) prior += warp_sum[i];
+      all += warp_sum[i];
+    }
+    if (g < groups) before[g] = total + prior + incl - n;
+    total += all;
+    __syncthreads();
+  }
+  const int n_live = total;
+  const LivePages L{bits, before, groups};
+  const int low = n_live < N ? L.rank(n_live) : n_live;  // live pages that stay
+  const int moved = n_live - low;
+  const long long stride = (long long)gridDim.x * kCopyThreads, first = (long long)blockIdx.x * kCopyThreads + threadIdx.x;
+  auto place = [&](int page) {  // where a page goes, -1 for a free one
+    if (!L.live(page)) return -1;
+    return page < n_live ? page : L.select(L.rank(page) - low, true);
+  };
+  for (long long i = first; i < N; i += stride) {
+    const int page = (int)i;
+    p.page_map[page] = place(page);
+    int r = 0;
+    if (page < n_live) r = L.live(page) ? p.refs[page] : p.refs[L.select(low + page - L.rank(page), false)];
+    p.refs_out[page] = r;
+  }
+  bool wrong = negative;
+  for (long long i = first; i < p.n_entries; i += stride) {
+    const int t = p.table[i];
+    wrong |= t >= N;
+    p.table_out[i] = t < 0 || t >= N ? -1 : place(t);
+  }
+  if (wrong) record_arg_error(ATTN_DEV_BAD_INDEX, SITE_PAGES_COMPACT);
+  if (first == 0) {
+    p.info[0] = n_live;
+    p.info[1] = moved;
+  }
+  const int per = p.c.chunk0[p.c.n];
+  const long long units = (long long)moved * p.c.n_layers * per;
+  for (long long u = blockIdx.x; u < units; u += gridDim.x) {
+    const long long r = u / per;
+    const int k = (int)(r / p.c.n_layers);
+    copy_chunk(p.c, L.select(low + k, false), L.select(k, true), p.c.page_size, (int)(r % p.c.n_layers), (int)(u % per));
+  }
+}
+
+// ------------------------------------------------------------------------------- fork
+
+struct ForkParams {
+  CacheBufs c;
+  int B, n_child, max_pages;
+  const int* table;
+  const int* lens;
+  const int* refs;
+  const int* parents;
+  const int* keep;
+  const int* new_lens;
+  int* table_out;
+  int* lens_out;
+  int* refs_out;
+  int* info;     // free pages left (or short of, below zero), status
+  // workspace
+  int* child;    // [n_child] pages kept | owner bit 31 ... see ForkChild
+  int* copies;   // [n_child][3] source, destination, tokens
+  int* fresh;    // [num_pages] free pages in rising order, as many as are taken
+  int* count;    // refs after, when they do not fit in shared memory
+  int* claim;
+  int* head;     // {copies, failed}
+};
+
+static constexpr int kForkThreads = 1024;
+
+// What a child keeps of its parent: tokens clamped as documented, whole pages, and whether it cuts a page.
+struct ForkKeep {
+  int parent, keep, full, held;
+  bool cut;
+};
+__device__ __forceinline__ ForkKeep fork_keep(const ForkParams& p, int c) {
+  ForkKeep k;
+  k.parent = p.parents[c];
+  const int old = k.parent >= 0 ? p.lens[k.parent] : 0, want = p.new_lens[c];
+  k.keep = max(0, min(min(p.keep[c], old), want));
+  k.full = k.keep / p.c.page_size;
+  k.cut = k.keep % p.c.page_size > 0;
+  k.held = (int)(((long long)want + p.c.page_size - 1) / p.c.page_size);
+  return k;
+}
+
+// Exclusive sum over the block of one value per thread; *total gets the block's sum.
+__device__ __forceinline__ int block_scan(int v, int* scratch, int* total) {
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  int incl = v;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int y = __shfl_up_sync(0xffffffffu, incl, o);
+    if (lane >= o) incl += y;
+  }
+  if (lane == 31) scratch[warp] = incl;
+  __syncthreads();
+  if (warp == 0) {
+    const int w = scratch[lane];
+    int x = w;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int y = __shfl_up_sync(0xffffffffu, x, o);
+      if (lane >= o) x += y;
+    }
+    scratch[lane] = x - w;
+    if (lane == 31) scratch[32] = x;
+  }
+  __syncthreads();
+  *total = scratch[32];
+  const int r = scratch[warp] + incl - v;
+  __syncthreads();
+  return r;
+}
+
+// The tables, in one CTA (the steps depend on one another through every page's count).  SMEM: counts and
+// claims in shared memory, else in the workspace.
+template <bool SMEM>
+__global__ void __launch_bounds__(kForkThreads) pages_fork_plan_kernel(const ForkParams p) {
+  extern __shared__ int fork_smem[];
+  __shared__ int scratch[33];
+  __shared__ int bad, n_copies;
+  const int N = p.c.num_pages, tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int page = p.c.page_size;
+  int* cnt = SMEM ? fork_smem : p.count;
+  int* claim = SMEM ? fork_smem + N : p.claim;
+  if (tid == 0) bad = n_copies = 0;
+  bool wrong = false;
+  for (int i = tid; i < N; i += kForkThreads) {
+    const int r = p.refs[i];
+    wrong |= r < 0;
+    cnt[i] = r;
+    claim[i] = 0x7fffffff;
+  }
+  __syncthreads();
+  // 1. Lengths and parents, before anything is indexed by them.
+  const long long cap = (long long)p.max_pages * page;
+  for (int b = tid; b < p.B; b += kForkThreads) wrong |= p.lens[b] < 0 || p.lens[b] > cap;
+  for (int c = tid; c < p.n_child; c += kForkThreads) {
+    const int a = p.parents[c];
+    wrong |= a < -1 || a >= p.B || p.new_lens[c] < 0 || p.new_lens[c] > cap;
+  }
+  if (wrong) bad = 1;
+  __syncthreads();
+  // 2. Every old reference goes (a warp per sequence; a count that is used up is a wrong one), then whole kept
+  // pages are referenced again.
+  if (!bad)
+    for (int b = warp; b < p.B; b += kForkThreads / 32) {
+      const int held = (int)(((long long)p.lens[b] + page - 1) / page);
+      for (int i = lane; i < held; i += 32) {
+        const int t = p.table[(long long)b * p.max_pages + i];
+        if (t < 0 || t >= N || atomicSub(&cnt[t], 1) < 1) wrong = true;
+      }
+    }
+  __syncthreads();  // nobody reads `bad` any more
+  if (wrong) bad = 1;
+  __syncthreads();
+  if (!bad)
+    for (int c = warp; c < p.n_child; c += kForkThreads / 32) {
+      const ForkKeep k = fork_keep(p, c);
+      for (int i = lane; i < k.full; i += 32) atomicAdd(&cnt[p.table[(long long)k.parent * p.max_pages + i]], 1);
+    }
+  __syncthreads();
+  // 3. A cut page nobody else holds goes to the first child that cuts it.
+  if (!bad)
+    for (int c = tid; c < p.n_child; c += kForkThreads) {
+      const ForkKeep k = fork_keep(p, c);
+      if (!k.cut) continue;
+      const int x = p.table[(long long)k.parent * p.max_pages + k.full];
+      if (cnt[x] == 0) atomicMin(&claim[x], c);
+    }
+  __syncthreads();
+  // 4. Pages each child needs, and where its run of fresh pages starts.
+  int total = 0;
+  if (!bad)
+    for (int c0 = 0; c0 < p.n_child; c0 += kForkThreads) {
+      const int c = c0 + tid;
+      int need = 0, own = 0;
+      if (c < p.n_child) {
+        const ForkKeep k = fork_keep(p, c);
+        if (k.cut) own = claim[p.table[(long long)k.parent * p.max_pages + k.full]] == c;
+        need = k.held - k.full - own;
+      }
+      int sum;
+      const int start = total + block_scan(need, scratch, &sum);
+      if (c < p.n_child) p.child[c] = start * 2 + own;  // start < 2^30: checked on the host
+      total += sum;
+    }
+  __syncthreads();
+  // 5. Owned pages count, then the free ones are listed (a warp per run of pages).
+  const int run = (N + 32 * 32 - 1) / (32 * 32) * 32;
+  const int r0 = min(warp * run, N), r1 = min(r0 + run, N);
+  int n = 0;
+  for (int i = r0 + lane; i < r1; i += 32) {
+    if (!bad && claim[i] != 0x7fffffff) cnt[i] = 1;
+    n += cnt[i] == 0;
+  }
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) n += __shfl_xor_sync(0xffffffffu, n, o);
+  int n_free;
+  int rank = block_scan(lane == 0 ? n : 0, scratch, &n_free);
+  rank = __shfl_sync(0xffffffffu, rank, 0);
+  const bool fail = bad || n_free < total;
+  if (!fail) {
+    for (int i0 = r0; i0 < r1 && rank < total; i0 += 32) {
+      const int i = i0 + lane;
+      const bool is_free = i < r1 && cnt[i] == 0;
+      const uint32_t m = __ballot_sync(0xffffffffu, is_free);
+      const int at = rank + __popc(m & ((1u << lane) - 1u));
+      if (is_free && at < total) {
+        p.fresh[at] = i;
+        cnt[i] = 1;
+      }
+      rank += __popc(m);
+    }
+  }
+  __syncthreads();
+  for (int i = tid; i < N; i += kForkThreads) p.refs_out[i] = fail ? p.refs[i] : cnt[i];
+  // 6. Cut pages that are copied.
+  for (int c = tid; c < p.n_child; c += kForkThreads) {
+    p.lens_out[c] = fail ? 0 : p.new_lens[c];
+    if (fail) continue;
+    const ForkKeep k = fork_keep(p, c);
+    const int x = p.child[c];
+    if (k.cut && !(x & 1)) {
+      const int at = atomicAdd(&n_copies, 1);
+      p.copies[at * 3] = p.table[(long long)k.parent * p.max_pages + k.full];
+      p.copies[at * 3 + 1] = p.fresh[x >> 1];
+      p.copies[at * 3 + 2] = k.keep % page;
+    }
+  }
+  __syncthreads();
+  if (tid == 0) {
+    p.info[0] = bad ? 0 : n_free - total;
+    p.info[1] = bad ? 1 : (fail ? 4 : 0);  // ATTN_ERR_INVALID_ARG, ATTN_ERR_BUDGET
+    p.head[0] = n_copies;
+    p.head[1] = fail;
+    if (bad) record_arg_error(ATTN_DEV_BAD_INDEX, SITE_PAGES_FORK);
+  }
+}
+
+// The new table's rows and the kept parts of cut pages, over the whole GPU.
+__global__ void __launch_bounds__(kCopyThreads) pages_fork_apply_kernel(const ForkParams p) {
+  const bool fail = p.head[1];
+  const int n_copies = p.head[0], per = p.c.chunk0[p.c.n];
+  const long long entries = (long long)p.n_child * p.max_pages;
+  for (long long i = (long long)blockIdx.x * kCopyThreads + threadIdx.x; i < entries;
+       i += (long long)gridDim.x * kCopyThreads) {
+    const int c = (int)(i / p.max_pages), j = (int)(i % p.max_pages);
+    int t = -1;
+    if (!fail) {
+      const ForkKeep k = fork_keep(p, c);
+      const int x = p.child[c], own = x & 1;
+      if (j < k.full + own) t = p.table[(long long)k.parent * p.max_pages + j];
+      else if (j < k.held) t = p.fresh[(x >> 1) + j - k.full - own];
+    }
+    p.table_out[i] = t;
+  }
+  const long long units = (long long)n_copies * p.c.n_layers * per;
+  for (long long u = blockIdx.x; u < units; u += gridDim.x) {
+    const long long r = u / per;
+    const int* e = p.copies + r / p.c.n_layers * 3;
+    copy_chunk(p.c, e[0], e[1], e[2], (int)(r % p.c.n_layers), (int)(u % per));
+  }
+}
+
+}  // namespace attn

@@ -50,6 +50,10 @@ enum WaitSite : int {
   SITE_TR_EPI = 58,
   SITE_TR_DRAIN = 59,
   SITE_TR_PAGE = 60,
+  SITE_ACCEPT = 70,
+  SITE_PAGES_COPY = 71,
+  SITE_PAGES_COMPACT = 72,
+  SITE_PAGES_FORK = 73,
 };
 
 // (code << 16) | site of the first error since the last reset; 0 when clean.

@@ -261,6 +261,71 @@ ATTN_API attn_status_t attn_decode_tree_paged(const void* q, const void* k_pool,
                                float* lse, void* ws, size_t ws_bytes, void* stream);
 
 /* ------------------------------------------------------------------------------------------
+ * Keeping a cache between decode calls, on the device alone (no read-back): the accepted path of a
+ * draft tree, and the pages of a paged cache ([COOPT] Opt-Pa, "lazy mapping"; [ORT-QSA] Code analysis 2).
+ *
+ * Common arguments.  k, v (16-byte aligned) and, for coded caches, float32 k_scale, v_scale (both or
+ * neither) hold n_layers layers one behind another: k, v [n_layers, num_pages, page_size, Hkv] rows of
+ * row_bytes bytes (D * 2 bf16, D E4M3 or INT8, D / 2 INT4; a multiple of 16), scales [n_layers,
+ * num_pages, page_size, Hkv].  All tables, lengths and counts are device int32.  Bad values among them are
+ * never used as an index: the call (attn_tree_accept: the sequence) is left undone and
+ * attn_device_status reports ATTN_ERR_INVALID_ARG with the site named below.
+ *
+ * attn_tree_accept — after attn_decode_tree: keep the accepted drafts.  path[b, 0 .. n_accepted[b] - 1]
+ * are drafts of sequence b (in [0, q_lens[b])); the cache rows of draft path[b, j], slot base + path[b, j]
+ * with base = kv_lens[b] - q_lens[b], become slot base + j in every layer, as if all rows were read
+ * before any is written (any order and repeats are allowed), and kv_lens_out[b] = base + n_accepted[b].
+ * page_table NULL: contiguous caches, num_pages is taken as B and page_size as Tmax; else [B, max_pages].
+ * The drafts' slots must lie in pages of one sequence only.  q_lens NULL: n_q everywhere.
+ * A sequence with a bad length, count, draft or page keeps its rows and kv_lens_out[b] = kv_lens[b] (site 70).
+ * kv_lens_out must not be kv_lens.
+ *
+ * attn_pages_copy — pages src[i] -> dst[i], i < n, in every layer.  No page may be written twice, nor be
+ * both written and read by different pairs (src[i] = dst[i] is allowed and does nothing): such a list,
+ * or one with a page outside the pool, moves nothing (site 71).
+ *
+ * attn_pages_fork — the next generation of sequences over a pool with shared pages.  Before: B sequences
+ * with rows of page_table [B, max_pages], kv_lens[b] tokens in ceil(kv_lens[b] / page_size) pages, and
+ * ref_counts[num_pages], the number of table rows that hold each page (plus what the caller pinned).
+ * After: child c continues parents[c] (-1: nobody) with its first keep = max(0, min(keep_lens[c],
+ * kv_lens[parent], new_lens[c])) tokens and has pages for new_lens[c].  So one call forks beams, cuts back
+ * rejected drafts, grows, ends (no child) and admits sequences.  Whole kept pages are shared.  A page cut
+ * by keep goes to the first child that cuts it if no child shares it whole and nobody pinned it; other children get its first
+ * keep % page_size tokens copied.  All other pages come from those nobody holds then, lowest first, in
+ * order of (child, page).  Out: table_out [n_children, max_pages] (-1 past a child's pages), lens_out =
+ * new_lens, refs_out [num_pages], info[2] = {free pages left, status}.  If pages are too few, status is
+ * ATTN_ERR_BUDGET and info[0] the shortage as a negative number; if a length, parent, table entry or
+ * count is bad, status is ATTN_ERR_INVALID_ARG (site 73).  In both cases nothing is copied, refs_out =
+ * ref_counts, lens_out = 0, table_out = -1: the old generation stands.  Outputs must not overlap inputs.
+ *
+ * attn_pages_compact — live pages (ref_counts > 0) at or past n_live, their number, move into the free ones
+ * below it, both in rising order.  page_map[p] is where page p went (itself if it stayed, -1 if free);
+ * table_out [B, max_pages] and refs_out [num_pages] are the table and counts in the new numbers (entries
+ * that are negative, free or outside the pool become -1, the last reported, as are negative counts, with
+ * site 72); info[2] = {n_live, pages moved}.  Outputs must not overlap inputs.
+ *
+ * Errors: ATTN_ERR_INVALID_ARG for bad sizes, null or misaligned pointers; ATTN_ERR_UNSUPPORTED for n_q > 64,
+ * more than 2^20 pages (copy, compact), 2^30 table entries.
+ * ------------------------------------------------------------------------------------------ */
+ATTN_API attn_status_t attn_tree_accept(void* k, void* v, float* k_scale, float* v_scale, int n_layers, int B, int Hkv,
+                               int row_bytes, const int* page_table, int max_pages, int page_size, int num_pages,
+                               const int* kv_lens, const int* q_lens, int n_q, const int* path, const int* n_accepted,
+                               int* kv_lens_out, void* stream);
+ATTN_API attn_status_t attn_pages_copy(void* k, void* v, float* k_scale, float* v_scale, int n_layers, int num_pages,
+                               int page_size, int Hkv, int row_bytes, const int* src, const int* dst, int n,
+                               void* stream);
+ATTN_API size_t attn_pages_fork_workspace_bytes(int n_children, int num_pages);
+ATTN_API attn_status_t attn_pages_fork(void* k, void* v, float* k_scale, float* v_scale, int n_layers, int num_pages,
+                               int page_size, int Hkv, int row_bytes, const int* page_table, const int* kv_lens,
+                               int B, int max_pages, const int* ref_counts, const int* parents, const int* keep_lens,
+                               const int* new_lens, int n_children, int* table_out, int* lens_out, int* refs_out,
+                               int* info, void* ws, size_t ws_bytes, void* stream);
+ATTN_API attn_status_t attn_pages_compact(void* k, void* v, float* k_scale, float* v_scale, int n_layers,
+                               int num_pages, int page_size, int Hkv, int row_bytes, const int* page_table, int B,
+                               int max_pages, const int* ref_counts, int* table_out, int* refs_out, int* page_map,
+                               int* info, void* stream);
+
+/* ------------------------------------------------------------------------------------------
  * attn_decode_splitkv_noalloc — the same split-KV decode, for callers that cannot allocate.
  *
  * The pages have no counterpart to this entry point; it is an integration aid.  Some callers
