@@ -9,6 +9,7 @@ from __future__ import annotations
 
 import contextlib
 import ctypes
+import functools
 import math
 import os
 
@@ -85,6 +86,8 @@ def _expect(name, t, dtypes, shape):
     if t is None:
         return
     if not isinstance(dtypes, tuple):
+        if t.dtype is dtypes and t.shape == shape and t.is_contiguous():
+            return
         dtypes = (dtypes,)
     if t.dtype not in dtypes or tuple(t.shape) != tuple(int(x) for x in shape) or not t.is_contiguous():
         want = "/".join(str(d).replace("torch.", "") for d in dtypes)
@@ -230,31 +233,55 @@ def _need_cuda(*ts):
             raise ValueError("device tensors expected (the library runs on the GPU only)")
 
 
-def _one_device(**ts):
+def _one_device(first, *ts):
     """Every tensor of the call on one CUDA device, which is returned."""
-    _need_cuda(*ts.values())
-    devs = {t.device for t in ts.values() if t is not None}
-    if len(devs) != 1:
-        raise ValueError(f"tensors on one device expected, got {sorted(map(str, devs))}")
-    return devs.pop()
+    device = first.device
+    for t in ts:
+        if t is not None and t.device != device:
+            _need_cuda(first, *ts)
+            raise ValueError("tensors on one device expected, got "
+                             f"{sorted({str(x.device) for x in (first, *ts) if x is not None})}")
+    if device.type != "cuda":
+        _need_cuda(first)
+    return device
 
 
-@contextlib.contextmanager
-def _on(device, stream):
-    """Make `device`, and `stream` when one is given, torch's current ones while outputs and workspace are
-    allocated and the call is made: memory from another stream's pool could be handed out again
-    while the kernels still use it.  Yields the stream to pass to the library."""
-    with contextlib.ExitStack() as ctx:
-        if device.index != torch.cuda.current_device():
-            ctx.enter_context(torch.cuda.device(device))
-        if stream is not None:
-            if not isinstance(stream, torch.cuda.Stream):
-                h = int(stream)
-                stream = torch.cuda.ExternalStream(h, device=device) if h else torch.cuda.default_stream(device)
-            if stream.device != device:
-                raise ValueError(f"stream: expected one of {device}, got one of {stream.device}")
-            ctx.enter_context(torch.cuda.stream(stream))
-        yield _stream(stream)
+class _On:
+    """Makes the call's device, and `stream` when one is given, torch's current ones while outputs and workspace
+    are allocated and the call is made: memory from another stream's pool could be handed out again
+    while the kernels still use it.  Yields the handle of the stream to pass to the library."""
+
+    __slots__ = ("device", "stream", "ctx")
+
+    def __init__(self, device, stream):
+        self.device, self.stream, self.ctx = device, stream, None
+
+    def __enter__(self):
+        device, stream = self.device, self.stream
+        if stream is None and device.index == torch.cuda.current_device():
+            return torch._C._cuda_getCurrentRawStream(device.index)
+        self.ctx = contextlib.ExitStack()
+        try:
+            self.ctx.enter_context(torch.cuda.device(device))
+            if stream is not None:
+                if not isinstance(stream, torch.cuda.Stream):
+                    h = int(stream)
+                    stream = torch.cuda.ExternalStream(h, device=device) if h else torch.cuda.default_stream(device)
+                if stream.device != device:
+                    raise ValueError(f"stream: expected one of {device}, got one of {stream.device}")
+                self.ctx.enter_context(torch.cuda.stream(stream))
+            return torch.cuda.current_stream().cuda_stream
+        except BaseException:
+            self.ctx.close()
+            raise
+
+    def __exit__(self, *exc):
+        if self.ctx is not None:
+            self.ctx.close()
+
+
+def _addr(t):
+    return None if t is None else t.data_ptr()
 
 
 def _bshd_strides(name, t, dtypes, shape):
@@ -430,10 +457,16 @@ def attn_decode_tree_workspace_bytes(B, Hq, Hkv, D, Tmax, n_q, scale=1.0) -> int
     return int(lib().attn_decode_tree_workspace_bytes(_dims(B, Hq, Hkv, D, scale), int(Tmax), int(n_q)))
 
 
+@functools.lru_cache(maxsize=256)
+def _tree_ws_bytes(device_index, B, Hq, Hkv, D, Tmax, n_q) -> int:
+    # The size goes by the current device's processors: the caller has made device_index current.
+    return int(lib().attn_decode_tree_workspace_bytes(_dims(B, Hq, Hkv, D, 1.0), min(Tmax, 2**31 - 1), n_q))
+
+
 def _decode_tree(name, q, k, v, kv_lens, tree_mask, q_lens, k_scale, v_scale, scale, o, lse, ws, want_lse, stream,
                  kv_dtype, page_table):
-    device = _one_device(q=q, k=k, v=v, kv_lens=kv_lens, tree_mask=tree_mask, q_lens=q_lens, k_scale=k_scale,
-                         v_scale=v_scale, page_table=page_table, o=o, lse=lse, ws=ws)
+    device = _one_device(q, k, v, kv_lens, tree_mask, q_lens, k_scale,
+                         v_scale, page_table, o, lse, ws)
     if q.dim() != 4 or k.dim() != 4:
         raise ValueError(f"q, k: expected 4 dimensions, got shapes {tuple(q.shape)} and {tuple(k.shape)}")
     B, n_q, Hq, D = q.shape
@@ -452,22 +485,24 @@ def _decode_tree(name, q, k, v, kv_lens, tree_mask, q_lens, k_scale, v_scale, sc
         _expect("page_table", page_table, torch.int32, (B, page_table.shape[1]))
         Tmax = page_table.shape[1] * k.shape[1]
     dims = _dims(B, Hq, Hkv, D, scale)
-    with _on(device, stream) as st:
+    with _On(device, stream) as st:
         if o is None:
-            o = torch.empty((B, n_q, Hq, D), dtype=torch.bfloat16, device=device)
+            o = torch.empty_like(q)
         if lse is None and want_lse:
-            lse = torch.empty((B, n_q, Hq), dtype=torch.float32, device=device)
+            lse = q.new_empty((B, n_q, Hq), dtype=torch.float32)
         if ws is None:
-            need = int(lib().attn_decode_tree_workspace_bytes(dims, min(Tmax, 2**31 - 1), n_q))
-            ws = torch.empty(need, dtype=torch.uint8, device=device) if need else None
-        tail = (_ptr(q_lens), _ptr(tree_mask))
-        out = (_ptr(o), _ptr(lse), _ptr(ws), 0 if ws is None else ws.numel() * ws.element_size(), st)
-        head = (_ptr(q), _ptr(k), _ptr(v), kind, _ptr(k_scale), _ptr(v_scale))
+            need = _tree_ws_bytes(device.index, B, Hq, Hkv, D, Tmax, n_q)
+            ws = q.new_empty(need, dtype=torch.uint8) if need else None
+        ws_bytes = 0 if ws is None else ws.numel() * ws.element_size()
         if page_table is None:
-            rc = lib().attn_decode_tree(*head, _ptr(kv_lens), *tail, Tmax, n_q, dims, *out)
+            rc = lib().attn_decode_tree(q.data_ptr(), k.data_ptr(), v.data_ptr(), kind, _addr(k_scale), _addr(v_scale),
+                                        kv_lens.data_ptr(), _addr(q_lens), tree_mask.data_ptr(), Tmax, n_q, dims,
+                                        o.data_ptr(), _addr(lse), _addr(ws), ws_bytes, st)
         else:
-            rc = lib().attn_decode_tree_paged(*head, _ptr(page_table), page_table.shape[1], k.shape[1], k.shape[0],
-                                              _ptr(kv_lens), *tail, n_q, dims, *out)
+            rc = lib().attn_decode_tree_paged(
+                q.data_ptr(), k.data_ptr(), v.data_ptr(), kind, _addr(k_scale), _addr(v_scale), page_table.data_ptr(),
+                page_table.shape[1], k.shape[1], k.shape[0], kv_lens.data_ptr(), _addr(q_lens), tree_mask.data_ptr(),
+                n_q, dims, o.data_ptr(), _addr(lse), _addr(ws), ws_bytes, st)
     _check(rc, name)
     return o, lse
 
@@ -502,14 +537,17 @@ def _cache(k, v, k_scale, v_scale):
         raise ValueError(f"k: expected a bf16 or one-byte code cache, got {k.dtype}")
     if coded != (k_scale is not None) or coded != (v_scale is not None):
         raise ValueError("k_scale, v_scale: expected for coded caches, and for them alone")
-    _expect("k", k, k.dtype, k.shape)
-    _expect("v", v, k.dtype, k.shape)
-    _expect("k_scale", k_scale, torch.float32, k.shape[:-1])
-    _expect("v_scale", v_scale, torch.float32, k.shape[:-1])
-    shape = k.shape if k.dim() == 5 else (1, *k.shape)
+    shape = tuple(k.shape)
+    _expect("k", k, k.dtype, shape)
+    _expect("v", v, k.dtype, shape)
+    if coded:
+        _expect("k_scale", k_scale, torch.float32, shape[:-1])
+        _expect("v_scale", v_scale, torch.float32, shape[:-1])
     if 0 in shape:
-        raise ValueError(f"k: expected a cache without empty dimensions, got {tuple(k.shape)}")
-    return shape[0], shape[1], shape[2], shape[3], shape[4] * k.element_size()
+        raise ValueError(f"k: expected a cache without empty dimensions, got {shape}")
+    layers = shape[0] if len(shape) == 5 else 1
+    pages, page_size, Hkv, row = shape[-4:]
+    return layers, pages, page_size, Hkv, row * (1 if coded else 2)
 
 
 def _table(page_table):
@@ -526,8 +564,8 @@ def attn_tree_accept(k, v, kv_lens, path, n_accepted, *, n_q: int | None = None,
     kv_lens[b] - q_lens[b] (q_lens None: n_q, which defaults to path.shape[1]).  k/v [layers, B, Tmax, Hkv, row] or
     pools [layers, num_pages, page_size, Hkv, row] with page_table [B, max_pages], or one layer without
     the first dimension -> kv_lens_out int32 [B]."""
-    device = _one_device(k=k, v=v, kv_lens=kv_lens, path=path, n_accepted=n_accepted, q_lens=q_lens,
-                         page_table=page_table, k_scale=k_scale, v_scale=v_scale, kv_lens_out=kv_lens_out)
+    device = _one_device(k, v, kv_lens, path, n_accepted, q_lens,
+                         page_table, k_scale, v_scale, kv_lens_out)
     layers, pages, page_size, Hkv, row = _cache(k, v, k_scale, v_scale)
     B = kv_lens.shape[0]
     n_q = path.shape[-1] if n_q is None else int(n_q)
@@ -540,15 +578,15 @@ def attn_tree_accept(k, v, kv_lens, path, n_accepted, *, n_q: int | None = None,
         raise ValueError(f"k/v: expected {B} sequences (the length of kv_lens), got {pages}")
     if page_table is not None and _table(page_table)[0] != B:
         raise ValueError(f"page_table: expected {B} rows, got {page_table.shape[0]}")
-    if kv_lens_out is not None and kv_lens_out.data_ptr() == kv_lens.data_ptr():
+    if kv_lens_out is not None and kv_lens_out.data_addr() == kv_lens.data_addr():
         raise ValueError("kv_lens_out: expected memory of its own, got kv_lens")
-    with _on(device, stream) as st:
+    with _On(device, stream) as st:
         if kv_lens_out is None:
             kv_lens_out = torch.empty_like(kv_lens)
-        rc = lib().attn_tree_accept(_ptr(k), _ptr(v), _ptr(k_scale), _ptr(v_scale), layers, B, Hkv, row,
-                                    _ptr(page_table), 0 if page_table is None else page_table.shape[1], page_size,
-                                    pages, _ptr(kv_lens), _ptr(q_lens), n_q, _ptr(path), _ptr(n_accepted),
-                                    _ptr(kv_lens_out), st)
+        rc = lib().attn_tree_accept(_addr(k), _addr(v), _addr(k_scale), _addr(v_scale), layers, B, Hkv, row,
+                                    _addr(page_table), 0 if page_table is None else page_table.shape[1], page_size,
+                                    pages, _addr(kv_lens), _addr(q_lens), n_q, _addr(path), _addr(n_accepted),
+                                    _addr(kv_lens_out), st)
     _check(rc, "attn_tree_accept")
     return kv_lens_out
 
@@ -556,14 +594,14 @@ def attn_tree_accept(k, v, kv_lens, path, n_accepted, *, n_q: int | None = None,
 def attn_pages_copy(k, v, src, dst, *, k_scale=None, v_scale=None, stream=None):
     """Copy pages src[i] -> dst[i] (int32 [n] on the device) of pools [layers, num_pages, page_size, Hkv, row]
     (or one layer), with their scale pools, in place."""
-    device = _one_device(k=k, v=v, src=src, dst=dst, k_scale=k_scale, v_scale=v_scale)
+    device = _one_device(k, v, src, dst, k_scale, v_scale)
     layers, pages, page_size, Hkv, row = _cache(k, v, k_scale, v_scale)
     n = src.numel()
     _expect("src", src, torch.int32, (n,))
     _expect("dst", dst, torch.int32, (n,))
-    with _on(device, stream) as st:
-        rc = lib().attn_pages_copy(_ptr(k), _ptr(v), _ptr(k_scale), _ptr(v_scale), layers, pages, page_size, Hkv, row,
-                                   _ptr(src), _ptr(dst), n, st)
+    with _On(device, stream) as st:
+        rc = lib().attn_pages_copy(_addr(k), _addr(v), _addr(k_scale), _addr(v_scale), layers, pages, page_size, Hkv, row,
+                                   _addr(src), _addr(dst), n, st)
     _check(rc, "attn_pages_copy")
 
 
@@ -579,9 +617,9 @@ def attn_pages_fork(k, v, page_table, kv_lens, ref_counts, parents, *, keep_lens
     nobody holds any more become free.  page_table int32 [B, max_pages], kv_lens int32 [B], ref_counts int32
     [num_pages] -> (page_table [n_children, max_pages], kv_lens [n_children], ref_counts [num_pages],
     info int32 [2] = free pages left, status), all new tensors; a status other than 0 (too few pages: budget;
-    bad arguments: invalid) leaves the old generation standing."""
-    device = _one_device(k=k, v=v, page_table=page_table, kv_lens=kv_lens, ref_counts=ref_counts, parents=parents,
-                         keep_lens=keep_lens, new_lens=new_lens, k_scale=k_scale, v_scale=v_scale, ws=ws)
+    bad arguments: invalid) leaves the old generation standing.  The new tensors are parts of one allocation."""
+    device = _one_device(k, v, page_table, kv_lens, ref_counts, parents,
+                         keep_lens, new_lens, k_scale, v_scale, ws)
     layers, pages, page_size, Hkv, row = _cache(k, v, k_scale, v_scale)
     B, max_pages = _table(page_table)
     n = parents.numel()
@@ -592,32 +630,37 @@ def attn_pages_fork(k, v, page_table, kv_lens, ref_counts, parents, *, keep_lens
     _expect("new_lens", new_lens, torch.int32, (n,))
     if ws is not None and not ws.is_contiguous():
         raise ValueError("ws: expected a contiguous workspace")
-    with _on(device, stream) as st:
-        out = [torch.empty(s, dtype=torch.int32, device=device) for s in ((n, max_pages), (n,), (pages,), (2,))]
-        if ws is None:
-            ws = torch.empty(attn_pages_fork_workspace_bytes(n, pages), dtype=torch.uint8, device=device)
-        rc = lib().attn_pages_fork(_ptr(k), _ptr(v), _ptr(k_scale), _ptr(v_scale), layers, pages, page_size, Hkv, row,
-                                   _ptr(page_table), _ptr(kv_lens), B, max_pages, _ptr(ref_counts), _ptr(parents),
-                                   _ptr(keep_lens), _ptr(new_lens), n, *map(_ptr, out), _ptr(ws),
-                                   ws.numel() * ws.element_size(), st)
+    with _On(device, stream) as st:
+        # One allocation for the outputs and the workspace, if it is not given: five cost as much as the launches.
+        need = 0 if ws is not None else attn_pages_fork_workspace_bytes(n, pages) // 4
+        sizes = (n * max_pages, n, pages, 2, need)
+        table, lens, refs, info, own_ws = ref_counts.new_empty(sum(sizes)).split_with_sizes(sizes)
+        out = table.view(n, max_pages), lens, refs, info
+        ws = own_ws if ws is None else ws
+        rc = lib().attn_pages_fork(_addr(k), _addr(v), _addr(k_scale), _addr(v_scale), layers, pages, page_size, Hkv, row,
+                                   _addr(page_table), _addr(kv_lens), B, max_pages, _addr(ref_counts), _addr(parents),
+                                   _addr(keep_lens), _addr(new_lens), n, table.data_ptr(), lens.data_ptr(),
+                                   refs.data_ptr(), info.data_ptr(), ws.data_ptr(), ws.numel() * ws.element_size(), st)
     _check(rc, "attn_pages_fork")
-    return tuple(out)
+    return out
 
 
 def attn_pages_compact(k, v, page_table, ref_counts, *, k_scale=None, v_scale=None, stream=None):
     """Move the live pages (ref_counts > 0) of a pool to its lowest page numbers, in place -> (page_table,
     ref_counts in the new numbers, page_map int32 [num_pages]: where each page went, -1 for free ones,
-    info int32 [2] = live pages, pages moved), all new tensors."""
-    device = _one_device(k=k, v=v, page_table=page_table, ref_counts=ref_counts, k_scale=k_scale, v_scale=v_scale)
+    info int32 [2] = live pages, pages moved), all new, parts of one allocation."""
+    device = _one_device(k, v, page_table, ref_counts, k_scale, v_scale)
     layers, pages, page_size, Hkv, row = _cache(k, v, k_scale, v_scale)
     B, max_pages = _table(page_table)
     _expect("ref_counts", ref_counts, torch.int32, (pages,))
-    with _on(device, stream) as st:
-        out = [torch.empty(s, dtype=torch.int32, device=device) for s in ((B, max_pages), (pages,), (pages,), (2,))]
-        rc = lib().attn_pages_compact(_ptr(k), _ptr(v), _ptr(k_scale), _ptr(v_scale), layers, pages, page_size, Hkv,
-                                      row, _ptr(page_table), B, max_pages, _ptr(ref_counts), *map(_ptr, out), st)
+    with _On(device, stream) as st:
+        sizes = (B * max_pages, pages, pages, 2)
+        table, refs, page_map, info = ref_counts.new_empty(sum(sizes)).split_with_sizes(sizes)
+        rc = lib().attn_pages_compact(_addr(k), _addr(v), _addr(k_scale), _addr(v_scale), layers, pages, page_size, Hkv,
+                                      row, _addr(page_table), B, max_pages, _addr(ref_counts), table.data_ptr(),
+                                      refs.data_ptr(), page_map.data_ptr(), info.data_ptr(), st)
     _check(rc, "attn_pages_compact")
-    return tuple(out)
+    return table.view(B, max_pages), refs, page_map, info
 
 
 NOALLOC_SCRATCH_BYTES = 4 << 20

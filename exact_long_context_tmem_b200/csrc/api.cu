@@ -423,6 +423,19 @@ static attn_status_t launch_decode_kind(attn_dtype_t kv, const void* q, const vo
   }
 }
 
+// Processors of the current device (asked for once per device).
+static int sm_count() {
+  static std::atomic<int> known[64];
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return 148;
+  int n = known[dev].load(std::memory_order_relaxed);
+  if (n == 0) {
+    if (cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess || n < 1) return 148;
+    known[dev].store(n, std::memory_order_relaxed);
+  }
+  return n;
+}
+
 // ---------------------------------------------------------------- tree decode
 
 // Row slots and ranges of a tree decode (tree.cuh): tps tokens per 128-row slot, two slots of rows per CTA
@@ -438,16 +451,13 @@ static TreePlan tree_plan(const attn_dims_t& d, int Tmax, int n_q) {
   const int slots = t.pair ? 2 : 1;
   t.n_rb = (n_q + t.tps * slots - 1) / (t.tps * slots);
   t.rows = 128 * slots;
-  int sms = 148, dev = 0;
-  if (cudaGetDevice(&dev) == cudaSuccess) cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
   const long long tiles = (long long)d.B * d.Hkv * (((long long)Tmax + 127) / 128);
-  t.n_groups = (int)std::max(1LL, std::min<long long>(std::max(sms, 1) / t.n_rb, tiles));
+  t.n_groups = (int)std::max(1LL, std::min<long long>(sm_count() / t.n_rb, tiles));
   return t;
 }
 
-static size_t tree_ws_bytes(const attn_dims_t& d, int Tmax, int n_q) {
+static size_t tree_ws_bytes(const attn_dims_t& d, int Tmax, const TreePlan& t) {
   if (Tmax <= 0 || d.B == 0) return 0;
-  const TreePlan t = tree_plan(d, Tmax, n_q);
   return (size_t)t.n_groups * t.n_rb * 2 * t.rows * (d.D + 1) * sizeof(float);
 }
 
@@ -512,9 +522,9 @@ static attn_status_t tree_call(const void* q, const void* k, const void* v, attn
       (long long)d.B * d.Hkv * (((long long)Tmax + 127) / 128) > 0x7fffffffLL ||
       (long long)d.B * d.Hq * n_q > 0x7fffffffLL)
     return ATTN_ERR_UNSUPPORTED;
-  const size_t need = tree_ws_bytes(d, Tmax, n_q);
-  if (need > 0 && (!ws || ws_bytes < need || !aligned16(ws))) return ATTN_ERR_INVALID_ARG;
   const TreePlan t = tree_plan(d, Tmax, n_q);
+  const size_t need = tree_ws_bytes(d, Tmax, t);
+  if (need > 0 && (!ws || ws_bytes < need || !aligned16(ws))) return ATTN_ERR_INVALID_ARG;
   TreeParams p{};
   p.B = d.B;
   p.Hq = d.Hq;
@@ -582,9 +592,7 @@ static attn_status_t cache_bufs(void* k, void* v, float* ks, float* vs, int n_la
 
 // CTAs for a number of 16 KB copy units: eight a processor keep HBM busy, fewer when there is less to do.
 static int copy_grid(long long units) {
-  int sms = 148, dev = 0;
-  if (cudaGetDevice(&dev) == cudaSuccess) cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
-  return (int)std::max(1LL, std::min<long long>(units, 8LL * std::max(sms, 1)));
+  return (int)std::max(1LL, std::min<long long>(units, 8LL * sm_count()));
 }
 
 // ---------------------------------------------------------------- diagnostics
@@ -867,7 +875,7 @@ attn_status_t attn_decode_multi(const void* q, const void* k, const void* v, att
 
 size_t attn_decode_tree_workspace_bytes(attn_dims_t dims, int Tmax, int n_q) {
   if (!dims_ok(dims) || dims.Hq / dims.Hkv > 128 || Tmax < 0 || n_q < 1 || n_q > 64) return 0;
-  return tree_ws_bytes(dims, Tmax, n_q);
+  return tree_ws_bytes(dims, Tmax, tree_plan(dims, Tmax, n_q));
 }
 
 attn_status_t attn_decode_tree(const void* q, const void* k, const void* v, attn_dtype_t kv_dtype,
