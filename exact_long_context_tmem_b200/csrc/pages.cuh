@@ -22,34 +22,103 @@ struct CacheBufs {
 };
 
 static constexpr int kCopyThreads = 256;
-static constexpr int kChunkBytes = kCopyThreads * 4 * 16;  // what a CTA has in flight
+static constexpr int kChunkBytes = kCopyThreads * 2 * 16;  // a CTA has two of them in flight
 static constexpr int kMaxPages = 1 << 20;                  // bitmaps of pages live in shared memory
 
-// One chunk of the first n_tok tokens of a page, src -> dst, in one layer.
-__device__ __forceinline__ void copy_chunk(const CacheBufs& c, int src, int dst, int n_tok, int layer, int chunk) {
-  int s = 0;
-  while (chunk >= c.chunk0[s + 1]) ++s;
-  const long long page = (long long)c.page_size * c.tok[s];
-  const long long bytes = (long long)n_tok * c.tok[s];
-  const long long off = (long long)(chunk - c.chunk0[s]) * kChunkBytes;
-  const char* from = c.p[s] + layer * c.layer[s] + src * page;
-  char* to = c.p[s] + layer * c.layer[s] + dst * page;
-  const long long end = min(bytes, off + kChunkBytes);
-  if (c.vec[s] == 16) {
-    uint4 x[4];
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const long long o = off + (threadIdx.x + i * kCopyThreads) * 16;
-      if (o < end) x[i] = *reinterpret_cast<const uint4*>(from + o);
+// Copies n_items runs of tokens in every layer: item(i, src, dst, n_tok) names the pages and how many tokens.
+// What bounds it is HBM.  Segments of up to four 8 KB chunks go round the CTAs of a grid of four per
+// processor (one chunk each when there are few); a CTA loads its next chunk before it stores the last.
+template <class Item>
+__device__ __forceinline__ void copy_items(const CacheBufs& c, long long n_items, Item item) {
+  struct Chunk {
+    const char* from;
+    char* to;
+    int bytes;
+    bool wide;
+  };
+  int seg0[5], per = 0;  // first segment of each buffer's page
+  long long seg_bytes = kChunkBytes;
+#pragma unroll 1
+  for (int r = 0; r < 2; ++r) {
+    per = 0;
+    for (int s = 0; s < c.n; ++s) {
+      seg0[s] = per;
+      per += (int)(((long long)c.page_size * c.tok[s] + seg_bytes - 1) / seg_bytes);
     }
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const long long o = off + (threadIdx.x + i * kCopyThreads) * 16;
-      if (o < end) *reinterpret_cast<uint4*>(to + o) = x[i];
+    if (r > 0 || n_items * c.n_layers * per < 16LL * gridDim.x) break;
+    seg_bytes = 4 * kChunkBytes;
+  }
+  const long long units = n_items * c.n_layers * per;
+  long long u = blockIdx.x;
+  if (u >= units) return;
+  const char* from = nullptr;  // the rest of the current segment
+  char* to = nullptr;
+  long long left = 0;
+  bool wide = true;
+  auto next = [&](Chunk& x) -> bool {
+    while (left <= 0) {
+      if (u >= units) return false;
+      int seg, s = 0, src, dst, n_tok, layer, i;
+      if (units <= 0xffffffffLL) {
+        const unsigned r = (unsigned)u / (unsigned)per;
+        seg = (int)((unsigned)u - r * (unsigned)per);
+        i = (int)(r / (unsigned)c.n_layers);
+        layer = (int)(r - (unsigned)i * (unsigned)c.n_layers);
+      } else {
+        seg = (int)(u % per);
+        layer = (int)(u / per % c.n_layers);
+        i = (int)(u / per / c.n_layers);
+      }
+      item(i, src, dst, n_tok);
+      while (s + 1 < c.n && seg >= seg0[s + 1]) ++s;
+      const long long page = (long long)c.page_size * c.tok[s], off = (seg - seg0[s]) * seg_bytes;
+      from = c.p[s] + layer * c.layer[s] + src * page + off;
+      to = c.p[s] + layer * c.layer[s] + dst * page + off;
+      left = src == dst ? 0 : min(seg_bytes, (long long)n_tok * c.tok[s] - off);
+      wide = c.vec[s] == 16;
+      u += gridDim.x;
     }
-  } else {
-    for (long long o = off + threadIdx.x * 4; o < end; o += kCopyThreads * 4)
-      *reinterpret_cast<uint32_t*>(to + o) = *reinterpret_cast<const uint32_t*>(from + o);
+    x.from = from;
+    x.to = to;
+    x.bytes = (int)min(left, (long long)kChunkBytes);
+    x.wide = wide;
+    from += kChunkBytes;
+    to += kChunkBytes;
+    left -= kChunkBytes;
+    return true;
+  };
+  auto load = [&](const Chunk& x, uint4(&v)[2]) {
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      const int o = (threadIdx.x + i * kCopyThreads) * 16;
+      if (x.wide && o < x.bytes) v[i] = *reinterpret_cast<const uint4*>(x.from + o);
+    }
+  };
+  auto store = [&](const Chunk& x, const uint4(&v)[2]) {
+    if (x.wide) {
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        const int o = (threadIdx.x + i * kCopyThreads) * 16;
+        if (o < x.bytes) *reinterpret_cast<uint4*>(x.to + o) = v[i];
+      }
+    } else {
+      for (int o = threadIdx.x * 4; o < x.bytes; o += kCopyThreads * 4)
+        *reinterpret_cast<uint32_t*>(x.to + o) = *reinterpret_cast<const uint32_t*>(x.from + o);
+    }
+  };
+  uint4 v[2], w[2];
+  Chunk a, b;
+  if (!next(a)) return;
+  load(a, v);
+  while (true) {
+    const bool second = next(b);
+    if (second) load(b, w);
+    store(a, v);
+    if (!second) break;
+    const bool more = next(a);
+    if (more) load(a, v);
+    store(b, w);
+    if (!more) break;
   }
 }
 
@@ -182,14 +251,11 @@ __global__ void __launch_bounds__(kCopyThreads) pages_copy_kernel(const CopyPara
     if (threadIdx.x == 0 && blockIdx.x == 0) record_arg_error(ATTN_DEV_BAD_INDEX, SITE_PAGES_COPY);
     return;
   }
-  const int per = p.c.chunk0[p.c.n];
-  const long long units = (long long)p.n * p.c.n_layers * per;
-  for (long long u = blockIdx.x; u < units; u += gridDim.x) {
-    const int chunk = (int)(u % per);
-    const long long r = u / per;
-    const int i = (int)(r / p.c.n_layers), a = p.src[i], d = p.dst[i];
-    if (a != d) copy_chunk(p.c, a, d, p.c.page_size, (int)(r % p.c.n_layers), chunk);
-  }
+  copy_items(p.c, p.n, [&](int i, int& src, int& dst, int& n_tok) {
+    src = p.src[i];
+    dst = p.dst[i];
+    n_tok = p.c.page_size;
+  });
 }
 
 // ------------------------------------------------------------------------------- compaction
@@ -338,13 +404,11 @@ __global__ void __launch_bounds__(kCopyThreads) pages_compact_kernel(const Compa
     p.info[0] = n_live;
     p.info[1] = moved;
   }
-  const int per = p.c.chunk0[p.c.n];
-  const long long units = (long long)moved * p.c.n_layers * per;
-  for (long long u = blockIdx.x; u < units; u += gridDim.x) {
-    const long long r = u / per;
-    const int k = (int)(r / p.c.n_layers);
-    copy_chunk(p.c, L.select(low + k, false), L.select(k, true), p.c.page_size, (int)(r % p.c.n_layers), (int)(u % per));
-  }
+  copy_items(p.c, moved, [&](int k, int& src, int& dst, int& n_tok) {
+    src = L.select(low + k, false);
+    dst = L.select(k, true);
+    n_tok = p.c.page_size;
+  });
 }
 
 // ------------------------------------------------------------------------------- fork
@@ -547,7 +611,7 @@ __global__ void __launch_bounds__(kForkThreads) pages_fork_plan_kernel(const For
 // The new table's rows and the kept parts of cut pages, over the whole GPU.
 __global__ void __launch_bounds__(kCopyThreads) pages_fork_apply_kernel(const ForkParams p) {
   const bool fail = p.head[1];
-  const int n_copies = p.head[0], per = p.c.chunk0[p.c.n];
+  const int n_copies = p.head[0];
   const long long entries = (long long)p.n_child * p.max_pages;
   for (long long i = (long long)blockIdx.x * kCopyThreads + threadIdx.x; i < entries;
        i += (long long)gridDim.x * kCopyThreads) {
@@ -561,12 +625,11 @@ __global__ void __launch_bounds__(kCopyThreads) pages_fork_apply_kernel(const Fo
     }
     p.table_out[i] = t;
   }
-  const long long units = (long long)n_copies * p.c.n_layers * per;
-  for (long long u = blockIdx.x; u < units; u += gridDim.x) {
-    const long long r = u / per;
-    const int* e = p.copies + r / p.c.n_layers * 3;
-    copy_chunk(p.c, e[0], e[1], e[2], (int)(r % p.c.n_layers), (int)(u % per));
-  }
+  copy_items(p.c, n_copies, [&](int i, int& src, int& dst, int& n_tok) {
+    src = p.copies[i * 3];
+    dst = p.copies[i * 3 + 1];
+    n_tok = p.copies[i * 3 + 2];
+  });
 }
 
 }  // namespace attn
