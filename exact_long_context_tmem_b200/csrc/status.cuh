@@ -50,6 +50,7 @@ enum WaitSite : int {
   SITE_TR_EPI = 58,
   SITE_TR_DRAIN = 59,
   SITE_TR_PAGE = 60,
+  SITE_TR_SCALE = 61,
   SITE_ACCEPT = 70,
   SITE_PAGES_COPY = 71,
   SITE_PAGES_COMPACT = 72,

@@ -619,8 +619,9 @@ __global__ void __launch_bounds__((TreeCfg<KIND, D, PAIR>::THREADS), 1)
         bool r = mbar_wait_warp<true>(&raw_full[rs], (u / C::NR) & 1, SITE_TR_CONV);
         r = r && mbar_wait_warp<true>(&u_empty[st], ((u / C::NU) & 1) ^ 1, SITE_TR_CONV);
         if (!r) return false;
-        const uint8_t* raw = smem + C::OFF_RAW + rs * C::RAW_BYTES;
-        uint8_t* dst = smem + C::OFF_U + st * C::TILE_BYTES;
+        // Shared addresses: through `smem`, which is aligned by hand, the accesses would be generic ones.
+        const uint32_t raw = smem_u32(smem + C::OFF_RAW) + rs * C::RAW_BYTES;
+        const uint32_t dst = smem_u32(smem + C::OFF_U) + st * C::TILE_BYTES;
 #pragma unroll 1
         for (int h = 0; h < 2; ++h) {
           uint32_t w4[4][4];
@@ -631,10 +632,10 @@ __global__ void __launch_bounds__((TreeCfg<KIND, D, PAIR>::THREADS), 1)
             col[i] = (sub & 3) + 4 * (hi_row ^ (i & 1));
             if constexpr (KIND == TREE_INT4) {
               col[i] ^= ((lane >> 3) & 1) << 2;  // rows are 64 bytes: the next row pair takes the other half
-              const uint2 x = *reinterpret_cast<const uint2*>(raw + row * 64 + col[i] * 8);
+              const uint2 x = lds_u2(raw + row * 64 + col[i] * 8);
               w4[i][0] = x.x, w4[i][1] = x.y, w4[i][2] = w4[i][3] = 0u;
             } else {
-              const uint4 x = *reinterpret_cast<const uint4*>(raw + row * 128 + col[i] * 16);
+              const uint4 x = lds_u4(raw + row * 128 + col[i] * 16);
               w4[i][0] = x.x, w4[i][1] = x.y, w4[i][2] = x.z, w4[i][3] = x.w;
             }
           }
@@ -643,10 +644,10 @@ __global__ void __launch_bounds__((TreeCfg<KIND, D, PAIR>::THREADS), 1)
             uint4 lo, hi;
             tree_widen<KIND>(w4[i], lo, hi);
             const int row = row0 + h * 16 + (i >> 1) * 8;
-            uint8_t* box = dst + (col[i] >> 2) * C::BOX_BYTES;
+            const uint32_t box = dst + (col[i] >> 2) * C::BOX_BYTES;
             const int ch = (col[i] & 3) * 2;
-            *reinterpret_cast<uint4*>(box + sw128_offset(row, ch)) = lo;
-            *reinterpret_cast<uint4*>(box + sw128_offset(row, ch + 1)) = hi;
+            sts_u4(box + sw128_offset(row, ch), lo);
+            sts_u4(box + sw128_offset(row, ch + 1), hi);
           }
         }
         const int kv0 = (it.t0 + j) * 128, base = it.len - it.qn;
@@ -656,7 +657,7 @@ __global__ void __launch_bounds__((TreeCfg<KIND, D, PAIR>::THREADS), 1)
           __syncwarp();
           if (d >= 0) {
             const bool drop = d >= it.qn || !((any >> d) & 1);
-            if (tree_scrub_row<C::NBOX, C::EXP_MASK>(dst, t, drop)) odd_piece[qi & 7] = qi + 1;
+            if (tree_scrub_row<C::NBOX, C::EXP_MASK>(smem + C::OFF_U + st * C::TILE_BYTES, t, drop)) odd_piece[qi & 7] = qi + 1;
           }
         }
         fence_proxy_async_smem();
@@ -786,6 +787,7 @@ __global__ void __launch_bounds__((TreeCfg<KIND, D, PAIR>::THREADS), 1)
     const int tok_i = (rb * C::NQ + (PAIR ? slot : 0)) * p.tps + r / p.G;  // this row's drafted token
     const int head_g = r % p.G;
     const bool row_used = r < p.tps * p.G && tok_i < p.n_q;
+    const bool warp_used = __any_sync(0xffffffffu, row_used);  // else its rows of S, P and O are nobody's
     int cs = 0, g = 0, qi = 0, ub = 0;  // tiles of this slot, tiles of the CTA, pieces, units before this piece
     bool ok = true;
     // The walk and its piece are kept in shared memory, a copy per warp: between pieces they are dead weight,
@@ -812,7 +814,20 @@ __global__ void __launch_bounds__((TreeCfg<KIND, D, PAIR>::THREADS), 1)
       unsigned long long m64 = 0;
       if (row_ok) m64 = (unsigned long long)__ldg(p.mask + (long long)it.b * p.n_q + tok_i) & tree_low_bits(it.qn);
       float m_used = -INFINITY, l = 0.f;
-      for (int j = PAIR ? 0 : slot; j < n; j += PAIR ? 1 : 2) {
+      if (CODED && !warp_used) {  // the tiles are only handed on
+        for (int j = PAIR ? 0 : slot; j < n && ok; j += PAIR ? 1 : 2) {
+          const int ss = (g + j) % (CODED ? C::NS : 1);
+          ok = mbar_wait_warp<true>(&s_full[slot], cs & 1, SITE_TR_SM_S) &&
+               mbar_wait_warp<true>(&sc_full[ss], ((g + j) / (CODED ? C::NS : 1)) & 1, SITE_TR_SM_SC);
+          if (ok && lane == 0) {
+            mbar_arrive(&p_full[slot]);
+            mbar_arrive(&sc_empty[ss]);
+          }
+          ++cs;
+        }
+        if (!ok) break;
+      }
+      for (int j = PAIR ? 0 : slot; j < n && (!CODED || warp_used); j += PAIR ? 1 : 2) {
         // tcgen05.ld/st are warp-collective: every lane takes the same branch around them.
         if (!(ok = mbar_wait_warp<true>(&s_full[slot], cs & 1, SITE_TR_SM_S))) break;
         tc_fence_after();

@@ -303,3 +303,44 @@ def test_empty_calls(cuda_device):
     o, lse = A.attn_decode_tree(q[:, :0], k, k, lens, mask[:, :0])
     assert o.shape == (2, 0, 4, 128) and lse.shape == (2, 0, 4)
     device_clean()
+
+
+@pytest.mark.parametrize("kind", ["fp8", "int8", "int4"])
+@pytest.mark.parametrize("n_q", [7, 40])
+@pytest.mark.parametrize("how", ["wide", "zeros", "negative", "one huge draft", "steep"])
+def test_scales_of_any_range(cuda_device, kind, n_q, how):
+    """V scales over 2^40, zero and negative scales, a draft whose scales are 2^60 of the others', K scales over 2^6
+    (scores up to 60 or so): the tolerance does not change, since a coded cache's products with V scales
+    and weights are each rounded to f16 (2^-11 of them, and of what is 2^-19 of a row's largest weight
+    2^-25 of that weight, 2^-9 of it at most over these 600 keys), together below the 2^-8 of a weight."""
+    g = torch.Generator().manual_seed(5)
+    d = make(kind, 3, n_q, 8, 2, [600, n_q, 333], 600, seed=4)
+    if how == "wide":
+        d["v_scale"] *= 2.0 ** torch.randint(-20, 21, d["v_scale"].shape, generator=g)
+    elif how == "zeros":
+        d["v_scale"] *= torch.randint(0, 2, d["v_scale"].shape, generator=g)
+        d["k_scale"] *= torch.randint(0, 2, d["k_scale"].shape, generator=g)
+    elif how == "negative":
+        d["v_scale"] *= torch.randint(0, 2, d["v_scale"].shape, generator=g) * 2 - 1
+        d["k_scale"] *= torch.randint(0, 2, d["k_scale"].shape, generator=g) * 2 - 1
+    elif how == "steep":
+        d["k_scale"] *= 2.0 ** torch.randint(-3, 4, d["k_scale"].shape, generator=g)
+    else:
+        for b, n in enumerate([600, n_q, 333]):
+            d["v_scale"][b, n - n_q + 2] *= 2.0**60
+    check(*tree(d, kind, cuda_device), d, kind)
+    device_clean()
+
+
+@pytest.mark.parametrize("kind", list(KINDS))
+def test_queries_of_any_size(cuda_device, kind):
+    """Queries times 2^60 with K scales (bf16: K) over 2^60, and a sequence whose queries are all zero."""
+    d = make(kind, 2, 9, 8, 2, [300, 200], 300, seed=9)
+    d["q"] *= 2.0**60
+    d["q"][1] = 0
+    if kind == "bf16":
+        d["k"] *= 2.0**-60
+    else:
+        d["k_scale"] *= 2.0**-60
+    check(*tree(d, kind, cuda_device), d, kind)
+    device_clean()
