@@ -211,7 +211,7 @@ struct TreeCfg {
   static constexpr int OFF_WALK = OFF_ML + (PAIR ? 0 : 2048);  // [8] walks, [8] pieces of the softmax warps
   static constexpr int OFF_BAR = OFF_WALK + 8 * (int)(sizeof(TreeWalk) + sizeof(TreePiece));
   static constexpr int N_BARS = 3 + 2 * NU + 2 * NR + 2 * NS + 2 + 2 + 2 + 2 + 1;
-  static constexpr int SMEM_BYTES = OFF_BAR + N_BARS * 8 + 64 + 1024;  // + walk start, flags, alignment slack
+  static constexpr int SMEM_BYTES = OFF_BAR + N_BARS * 8 + 72 + 1024;  // + walk start, flags, alignment slack
   static constexpr int THREADS = CODED ? 512 : 384;
   // bf16: the softmax holds a row's 128 scores in registers; the control warpgroup gives up what that
   // takes (the sum never exceeds what the launch holds: checked on the host before the first launch).
@@ -376,6 +376,7 @@ __global__ void __launch_bounds__((TreeCfg<KIND, D, PAIR>::THREADS), 1)
   // ring of units ahead of the epilogue that asks (NU <= 6, two units or more a piece): eight entries.
   int* odd_piece = walk0 + 3;
   uint32_t* q_max = reinterpret_cast<uint32_t*>(odd_piece + 8);  // [4] largest |q| (bf16 bits) per converter warp
+  float* q_down = reinterpret_cast<float*>(q_max + 4);  // what undoes the queries' power of two
 
   const int warp = threadIdx.x >> 5;
   const int lane = threadIdx.x & 31;
@@ -384,7 +385,7 @@ __global__ void __launch_bounds__((TreeCfg<KIND, D, PAIR>::THREADS), 1)
   if (threadIdx.x == 0) {
     mbar_init(q_full, CODED ? 4 : 1);
     mbar_init(q_raw, 1);
-    mbar_init(q_empty, 1);
+    mbar_init(q_empty, CODED ? 3 : 1);  // the MMA is done with the queries, and the scale warps with q_down
     for (int i = 0; i < C::NU; ++i) {
       mbar_init(&u_full[i], CODED ? 4 : 1);  // converter warps, or the producer's expect_tx
       mbar_init(&u_empty[i], 1);
@@ -394,7 +395,7 @@ __global__ void __launch_bounds__((TreeCfg<KIND, D, PAIR>::THREADS), 1)
       mbar_init(&raw_empty[i], 4);
     }
     for (int i = 0; i < C::NS; ++i) {
-      mbar_init(&sc_full[i], 4);
+      mbar_init(&sc_full[i], 2);
       mbar_init(&sc_empty[i], PAIR ? 8 : 4);
     }
     for (int s = 0; s < 2; ++s) {
@@ -600,7 +601,63 @@ __global__ void __launch_bounds__((TreeCfg<KIND, D, PAIR>::THREADS), 1)
     }
     __syncwarp();
   } else if (warp < 4) {
-    if constexpr (!CODED) regs_dec<C::REGS_CTRL>();
+    if constexpr (!CODED) {
+      regs_dec<C::REGS_CTRL>();
+    } else {
+      // ------------------------------------------------------------------ scales
+      // Lane l of the two warps stages tokens t0 and t0 + 64 of each tile, loaded one tile ahead.
+      const int t0 = (warp - 2) * 32 + lane;
+      int g = 0, qi = 0;
+      bool ok = true;
+      float ks[2], vs[2];
+      auto fetch = [&](const TreePiece& it, int j) {
+#pragma unroll
+        for (int x = 0; x < 2; ++x) {
+          const int tok = (it.t0 + j) * 128 + t0 + 64 * x;
+          ks[x] = vs[x] = 0.f;
+          if (tok < it.len) {
+            const int pg = tree_page(p, it.b, tok);
+            if (pg >= 0) {
+              const long long row = ((long long)pg * p.page_size + tree_page_off(p, tok)) * p.Hkv + it.kvh;
+              ks[x] = __ldg(p.k_scale + row);
+              vs[x] = __ldg(p.v_scale + row);
+            }
+          }
+        }
+      };
+      TreeWalk w;
+      TreePiece it;
+      w.init(p, walk0);
+      while (ok && w.next(p, it)) {
+        fetch(it, 0);
+        if (!(ok = mbar_wait_warp<true>(q_full, qi & 1, SITE_TR_SCALE))) break;
+        const float kf = p.scale_log2 * *q_down;
+        __syncwarp();
+        if (lane == 0) mbar_arrive(q_empty);
+        for (int j = 0; j < it.n; ++j) {
+          const int ss = g % C::NS;
+          if (!(ok = mbar_wait_warp<true>(&sc_empty[ss], ((g / C::NS) & 1) ^ 1, SITE_TR_SCALE))) break;
+          float* dst = reinterpret_cast<float*>(smem + C::OFF_SC + ss * C::SC_BYTES);
+#pragma unroll
+          for (int x = 0; x < 2; ++x) {
+            const int t = t0 + 64 * x, tok = (it.t0 + j) * 128 + t;
+            // A draft's scale may be anything; the rows that do not see it must not meet it.
+            if (tok >= it.len - it.qn && !(fabsf(vs[x]) <= 3.4028234663852886e38f)) {
+              vs[x] = 0.f;
+              if (tok < it.len) odd_piece[qi & 7] = qi + 1;
+            }
+            dst[t] = ks[x] * kf;
+            dst[128 + t] = vs[x];
+            dst[256 + t] = fminf(fmaxf(__log2f(fabsf(vs[x])), -100.f), 100.f);
+          }
+          if (j + 1 < it.n) fetch(it, j + 1);
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&sc_full[ss]);
+          ++g;
+        }
+        ++qi;
+      }
+    }
   } else if (CODED && warp >= 12) {
     // ------------------------------------------------------------------ converters
     if constexpr (CODED) {
@@ -612,7 +669,7 @@ __global__ void __launch_bounds__((TreeCfg<KIND, D, PAIR>::THREADS), 1)
       // cache (4.3 of 17 stall cycles an instruction, 8400 cycles a tile against 1450 of HBM time).
       const int sub = lane & 7, hi_row = sub >> 2;
       const int row0 = cw * 32 + (lane >> 3) * 2 + hi_row;
-      int u = 0, g = 0, qi = 0;
+      int u = 0, qi = 0;
       bool ok = true;
       auto convert = [&](const TreePiece& it, int j, bool is_v) -> bool {
         const int rs = u % C::NR, st = u % C::NU;
@@ -625,17 +682,17 @@ __global__ void __launch_bounds__((TreeCfg<KIND, D, PAIR>::THREADS), 1)
 #pragma unroll 1
         for (int h = 0; h < 2; ++h) {
           uint32_t w4[4][4];
-          int col[4];
+          int col[2];
 #pragma unroll
           for (int i = 0; i < 4; ++i) {  // rows row0 + 16 h + 8 (i >> 1), both halves of their columns
             const int row = row0 + h * 16 + (i >> 1) * 8;
-            col[i] = (sub & 3) + 4 * (hi_row ^ (i & 1));
+            if (i < 2) col[i] = (sub & 3) + 4 * (hi_row ^ i);
             if constexpr (KIND == TREE_INT4) {
-              col[i] ^= ((lane >> 3) & 1) << 2;  // rows are 64 bytes: the next row pair takes the other half
-              const uint2 x = lds_u2(raw + row * 64 + col[i] * 8);
+              if (i < 2) col[i] ^= ((lane >> 3) & 1) << 2;  // rows are 64 bytes: the next row pair takes the other half
+              const uint2 x = lds_u2(raw + row * 64 + col[i & 1] * 8);
               w4[i][0] = x.x, w4[i][1] = x.y, w4[i][2] = w4[i][3] = 0u;
             } else {
-              const uint4 x = lds_u4(raw + row * 128 + col[i] * 16);
+              const uint4 x = lds_u4(raw + row * 128 + col[i & 1] * 16);
               w4[i][0] = x.x, w4[i][1] = x.y, w4[i][2] = x.z, w4[i][3] = x.w;
             }
           }
@@ -644,8 +701,8 @@ __global__ void __launch_bounds__((TreeCfg<KIND, D, PAIR>::THREADS), 1)
             uint4 lo, hi;
             tree_widen<KIND>(w4[i], lo, hi);
             const int row = row0 + h * 16 + (i >> 1) * 8;
-            const uint32_t box = dst + (col[i] >> 2) * C::BOX_BYTES;
-            const int ch = (col[i] & 3) * 2;
+            const uint32_t box = dst + (col[i & 1] >> 2) * C::BOX_BYTES;
+            const int ch = (col[i & 1] & 3) * 2;
             sts_u4(box + sw128_offset(row, ch), lo);
             sts_u4(box + sw128_offset(row, ch + 1), hi);
           }
@@ -669,9 +726,6 @@ __global__ void __launch_bounds__((TreeCfg<KIND, D, PAIR>::THREADS), 1)
         ++u;
         return true;
       };
-      // Scales of a tile: thread t loads those of token t one tile ahead.
-      float ks = 0.f, vs = 0.f;
-      float q_down = 1.f;  // what undoes the queries' power of two
       // The piece's queries, bf16 -> f16 in place, times a power of two that takes the largest |q| to
       // [2^14, 2^15).  What falls below f16's normal range is then off by at most 2^-39 of the largest,
       // far less than fp32 accumulation loses on it.
@@ -698,7 +752,7 @@ __global__ void __launch_bounds__((TreeCfg<KIND, D, PAIR>::THREADS), 1)
         top = max(max(q_max[0], q_max[1]), max(q_max[2], q_max[3]));
         const int shift = min(14 + 127 - max((int)(top >> 7), 1), 127);
         const float up = __uint_as_float((uint32_t)(127 + shift) << 23);
-        q_down = exp2f((float)-shift);
+        if (t == 0) *q_down = exp2f((float)-shift);
         for (int i = t; i < CHUNKS; i += 128) {
           if (((i >> 3) & 127) >= rows) continue;
           const uint4 x = qs[i];
@@ -721,43 +775,11 @@ __global__ void __launch_bounds__((TreeCfg<KIND, D, PAIR>::THREADS), 1)
         if (lane == 0) mbar_arrive(q_full);
         return true;
       };
-      auto fetch = [&](const TreePiece& it, int j) {
-        const int tok = (it.t0 + j) * 128 + t;
-        ks = vs = 0.f;
-        if (tok < it.len) {
-          const int pg = tree_page(p, it.b, tok);
-          if (pg >= 0) {
-            const long long row = ((long long)pg * p.page_size + tree_page_off(p, tok)) * p.Hkv + it.kvh;
-            ks = __ldg(p.k_scale + row);
-            vs = __ldg(p.v_scale + row);
-          }
-        }
-      };
-      auto scales = [&](const TreePiece& it, int j, bool prefetch) -> bool {
-        const int ss = g % C::NS;
-        if (!mbar_wait_warp<true>(&sc_empty[ss], ((g / C::NS) & 1) ^ 1, SITE_TR_CONV)) return false;
-        float* dst = reinterpret_cast<float*>(smem + C::OFF_SC + ss * C::SC_BYTES);
-        const int tok = (it.t0 + j) * 128 + t;
-        // A draft's scale may be anything; the rows that do not see it must not meet it.
-        if (tok >= it.len - it.qn && !(fabsf(vs) <= 3.4028234663852886e38f)) {
-          vs = 0.f;
-          if (tok < it.len) odd_piece[qi & 7] = qi + 1;
-        }
-        dst[t] = ks * p.scale_log2 * q_down;
-        dst[128 + t] = vs;
-        dst[256 + t] = fminf(fmaxf(__log2f(fabsf(vs)), -100.f), 100.f);
-        if (prefetch) fetch(it, j + 1);
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&sc_full[ss]);
-        ++g;
-        return true;
-      };
       TreeWalk w;
       TreePiece it;
       w.init(p, walk0);
       while (ok && w.next(p, it)) {
         const int n = it.n;
-        fetch(it, 0);
         ok = convert_q();
         for (int x = 0; x < 2 * n && ok; ++x) {  // the units of the piece, in the order of tree_v_unit
           bool is_v;
@@ -769,8 +791,7 @@ __global__ void __launch_bounds__((TreeCfg<KIND, D, PAIR>::THREADS), 1)
             is_v = x == 2 * n - 1 || (x > 0 && !(x & 1));
             j = x == 2 * n - 1 ? n - 1 : is_v ? (x - 2) >> 1 : (x + 1) >> 1;
           }
-          if (!is_v) ok = scales(it, j, j + 1 < n);
-          ok = ok && convert(it, j, is_v);
+          ok = convert(it, j, is_v);
         }
         ++qi;
       }
@@ -811,8 +832,11 @@ __global__ void __launch_bounds__((TreeCfg<KIND, D, PAIR>::THREADS), 1)
     while (ok && next_piece(qi == 0)) {
       const int n = it.n, t0 = it.t0, base = it.len - it.qn;
       const bool row_ok = row_used && tok_i < it.qn;
-      unsigned long long m64 = 0;
-      if (row_ok) m64 = (unsigned long long)__ldg(p.mask + (long long)it.b * p.n_q + tok_i) & tree_low_bits(it.qn);
+      // This row's mask, read where it is needed (the last tiles of a sequence): no registers in the loop.
+      auto row_mask = [&]() -> unsigned long long {
+        if (!row_ok) return 0;
+        return (unsigned long long)__ldg(p.mask + (long long)it.b * p.n_q + tok_i) & tree_low_bits(it.qn);
+      };
       float m_used = -INFINITY, l = 0.f;
       if (CODED && !warp_used) {  // the tiles are only handed on
         for (int j = PAIR ? 0 : slot; j < n && ok; j += PAIR ? 1 : 2) {
@@ -841,7 +865,7 @@ __global__ void __launch_bounds__((TreeCfg<KIND, D, PAIR>::THREADS), 1)
           return *reinterpret_cast<uint32_t(*)[CH]>(&sr[(CODED ? c & 1 : c) * CH]);
         };
         auto mask_chunk = [&](int c, uint32_t(&x)[CH]) {
-          const uint32_t see = tree_seen_word(c * CH, kv0, base, m64);
+          const uint32_t see = tree_seen_word(c * CH, kv0, base, row_mask());
 #pragma unroll
           for (int i = 0; i < CH; ++i)
             if (!((see >> i) & 1u)) x[i] = __float_as_uint(-INFINITY);
@@ -926,9 +950,9 @@ __global__ void __launch_bounds__((TreeCfg<KIND, D, PAIR>::THREADS), 1)
         const float neg_m = (m_used == -INFINITY) ? 0.f : -m_used;
         const float2 c2 = make_float2(p.scale_log2, p.scale_log2);
         const float2 nm2 = make_float2(neg_m, neg_m);
-        float2 a0 = make_float2(0.f, 0.f), a1 = a0, a2 = a0, a3 = a0;  // the row sum, of the unrounded weights
+        float2 a0 = make_float2(0.f, 0.f), a1 = a0;  // the row sum, of the unrounded weights
         auto add_sum = [&](int i, float2 e) {
-          float2& a = (i & 3) == 0 ? a0 : (i & 3) == 1 ? a1 : (i & 3) == 2 ? a2 : a3;
+          float2& a = (i & 1) == 0 ? a0 : a1;
           a = add2(a, e);
         };
         if constexpr (CODED) {
@@ -1020,7 +1044,7 @@ __global__ void __launch_bounds__((TreeCfg<KIND, D, PAIR>::THREADS), 1)
           for (int i = 0; i < 64; ++i)
             add_sum(i, make_float2(__uint_as_float(sr[2 * i]), __uint_as_float(sr[2 * i + 1])));
         }
-        a0 = add2(add2(a0, a1), add2(a2, a3));
+        a0 = add2(a0, a1);
         l += a0.x + a0.y;
         ++cs;
       }
@@ -1082,7 +1106,8 @@ __global__ void __launch_bounds__((TreeCfg<KIND, D, PAIR>::THREADS), 1)
           float out[32];
 #pragma unroll
           for (int i = 0; i < 32; ++i) out[i] = __uint_as_float(ov[tree_place<KIND>(i)]);
-          if (fix && lse2 != -INFINITY) {  // non-finite values of the drafts this row sees
+          if (fix && lse2 != -INFINITY) {
+            const unsigned long long m64 = row_mask();  // non-finite values of the drafts this row sees
 #pragma unroll 1
             for (int dq = 0; dq < it.qn; ++dq) {
               const int tok = base + dq;
