@@ -207,20 +207,24 @@ struct TreeCfg {
   static constexpr int OFF_U = OFF_Q + NQ * TILE_BYTES;
   static constexpr int OFF_RAW = OFF_U + NU * TILE_BYTES;
   static constexpr int OFF_SC = OFF_RAW + NR * RAW_BYTES;      // [NS][3][128] floats
-  static constexpr int OFF_ML = OFF_SC + NS * 1536;            // [2 slots][128] (max, sum) of the halves
+  static constexpr int OFF_ML = OFF_SC + NS * (1536 + 32);            // [2 slots][128] (max, sum) of the halves
   static constexpr int OFF_WALK = OFF_ML + (PAIR ? 0 : 2048);  // [8] walks, [8] pieces of the softmax warps
   static constexpr int OFF_BAR = OFF_WALK + 8 * (int)(sizeof(TreeWalk) + sizeof(TreePiece));
   static constexpr int N_BARS = 3 + 2 * NU + 2 * NR + 2 * NS + 2 + 2 + 2 + 2 + 1;
   static constexpr int SMEM_BYTES = OFF_BAR + N_BARS * 8 + 72 + 1024;  // + walk start, flags, alignment slack
   static constexpr int THREADS = CODED ? 512 : 384;
-  // bf16: the softmax holds a row's 128 scores in registers; the control warpgroup gives up what that
-  // takes (the sum never exceeds what the launch holds: checked on the host before the first launch).
-  // Coded caches need no split: there the softmax reads the scores from TMEM twice, 32 at a time.
-  static constexpr int REGS_CTRL = 72;
-  static constexpr int REGS_SOFTMAX = 216;
-  static constexpr int REGS_TOTAL = CODED ? 0 : REGS_CTRL * 128 + REGS_SOFTMAX * 256;
+  // Register split: the softmax holds a row's 128 scores (bf16) or half of them (coded caches, of whose 512
+  // threads a launch has 128 registers each), and the other warpgroups give up what that takes.  The sum
+  // never exceeds what the launch holds (checked on the host before the first launch).  Nothing in a loop may
+  // spill: next to 200 KB of shared memory there is hardly any L1, and a reload takes some 300 cycles.
+  static constexpr int REGS_CTRL = CODED ? 96 : 104;  // the MMA issuer of two row slots needs them
+  static constexpr int REGS_CONV = 96;
+  static constexpr int REGS_SOFTMAX = CODED ? 160 : 200;
+  static constexpr int REGS_TOTAL = (REGS_CTRL + (CODED ? REGS_CONV : 0) + 2 * REGS_SOFTMAX) * 128;
   static constexpr uint32_t EXP_MASK = CODED ? 0x7c00u : 0x7f80u;  // exponent field of an MMA operand
-  static constexpr int SC_BYTES = 3 * 512;  // scales of a tile: K (times all score factors), V, log2 |V|
+  // Scales of a tile: K (times all score factors), V, log2 |V|, then from either scale warp, for its 64 tokens, the
+  // largest and smallest of K's and of the logarithms.
+  static constexpr int SC_BYTES = 3 * 512 + 32;
   static constexpr uint32_t TMEM_COLS = 512;
   static constexpr float RESCALE_THRESHOLD = 8.0f;
   static constexpr int ROWS = PAIR ? 256 : 128;  // rows of a partial
@@ -422,7 +426,7 @@ __global__ void __launch_bounds__((TreeCfg<KIND, D, PAIR>::THREADS), 1)
 
   if (warp == 0) {
     // ------------------------------------------------------------------ TMA producer
-    if constexpr (!CODED) regs_dec<C::REGS_CTRL>();
+    regs_dec<C::REGS_CTRL>();
     if (lane == 0) {
       tma_prefetch_desc(&tmQ);
       tma_prefetch_desc(&tmK);
@@ -484,7 +488,7 @@ __global__ void __launch_bounds__((TreeCfg<KIND, D, PAIR>::THREADS), 1)
     __syncwarp();
   } else if (warp == 1) {
     // ------------------------------------------------------------------ MMA issuer
-    if constexpr (!CODED) regs_dec<C::REGS_CTRL>();
+    regs_dec<C::REGS_CTRL>();
     {
       constexpr uint32_t idesc_qk = make_idesc_f16(128, 128, false, false, !CODED);
       constexpr uint32_t idesc_pv = make_idesc_f16(128, D, false, true, !CODED);
@@ -601,9 +605,8 @@ __global__ void __launch_bounds__((TreeCfg<KIND, D, PAIR>::THREADS), 1)
     }
     __syncwarp();
   } else if (warp < 4) {
-    if constexpr (!CODED) {
-      regs_dec<C::REGS_CTRL>();
-    } else {
+    regs_dec<C::REGS_CTRL>();
+    if constexpr (CODED) {
       // ------------------------------------------------------------------ scales
       // Lane l of the two warps stages tokens t0 and t0 + 64 of each tile, loaded one tile ahead.
       const int t0 = (warp - 2) * 32 + lane;
@@ -650,6 +653,28 @@ __global__ void __launch_bounds__((TreeCfg<KIND, D, PAIR>::THREADS), 1)
             dst[128 + t] = vs[x];
             dst[256 + t] = fminf(fmaxf(__log2f(fabsf(vs[x])), -100.f), 100.f);
           }
+          uint32_t k1 = 0, k0 = 0x7f800000u, v1 = 0, v0 = 0x7f800000u;
+          bool odd = false;  // K scales that are negative or not finite
+#pragma unroll
+          for (int x = 0; x < 2; ++x) {
+            const float k = ks[x] * kf;
+            odd |= !(k >= 0.f && k <= 3.4028234663852886e38f);
+            k1 = max(k1, __float_as_uint(k));
+            k0 = min(k0, __float_as_uint(k));
+            v1 = max(v1, __float_as_uint(fabsf(vs[x])));
+            v0 = min(v0, __float_as_uint(fabsf(vs[x])));
+          }
+          k1 = __reduce_max_sync(0xffffffffu, k1);
+          k0 = __reduce_min_sync(0xffffffffu, k0);
+          v1 = __reduce_max_sync(0xffffffffu, v1);
+          v0 = __reduce_min_sync(0xffffffffu, v0);
+          odd = __any_sync(0xffffffffu, odd);
+          if (lane == 0) {
+            dst[384 + (warp - 2) * 4] = __uint_as_float(k1);
+            dst[385 + (warp - 2) * 4] = odd ? -INFINITY : __uint_as_float(k0);
+            dst[386 + (warp - 2) * 4] = fminf(fmaxf(__log2f(__uint_as_float(v1)), -100.f), 100.f);
+            dst[387 + (warp - 2) * 4] = fminf(fmaxf(__log2f(__uint_as_float(v0)), -100.f), 100.f);
+          }
           if (j + 1 < it.n) fetch(it, j + 1);
           __syncwarp();
           if (lane == 0) mbar_arrive(&sc_full[ss]);
@@ -661,6 +686,7 @@ __global__ void __launch_bounds__((TreeCfg<KIND, D, PAIR>::THREADS), 1)
   } else if (CODED && warp >= 12) {
     // ------------------------------------------------------------------ converters
     if constexpr (CODED) {
+      regs_dec<C::REGS_CONV>();
       const int cw = warp - 12, t = cw * 32 + lane;
       // Lane l of a warp widens 16 codes: row pair 2 (l >> 3) + ((l >> 2) & 1) of eight rows, 16-code column c.  The
       // two rows of a pair take columns 0-3 and 4-7, so the eight lanes of a phase read 128 distinct
@@ -798,7 +824,7 @@ __global__ void __launch_bounds__((TreeCfg<KIND, D, PAIR>::THREADS), 1)
     }
   } else {
     // ------------------------------------------------------------------ softmax + epilogue
-    if constexpr (!CODED) regs_inc<C::REGS_SOFTMAX>();
+    regs_inc<C::REGS_SOFTMAX>();
     const int slot = (warp - 4) >> 2;
     const int wq = warp & 3;  // TMEM lane quarter this warp may access
     const int r = wq * 32 + lane;
@@ -857,10 +883,11 @@ __global__ void __launch_bounds__((TreeCfg<KIND, D, PAIR>::THREADS), 1)
         tc_fence_after();
         const int kv0 = (t0 + j) * 128;
         const bool edge = kv0 + 128 > base;
-        // bf16: sr holds the row's 128 scores, read as four chunks of 32; coded caches: two chunks of 16, chunk
-        // c in sr + 16 (c & 1).
+        // bf16: sr holds the row's 128 scores, read as four chunks of 32.  Coded caches: half of them for the
+        // maximum, then two chunks of 16 in turn for the weights; longer loop bodies, of which there are several
+        // kinds in flight at once, run out of the instruction cache.
         constexpr int CH = CODED ? 16 : 32;
-        uint32_t sr[CODED ? 32 : 128];
+        uint32_t sr[CODED ? 64 : 128];
         auto chunk = [&](int c) -> uint32_t(&)[CH] {
           return *reinterpret_cast<uint32_t(*)[CH]>(&sr[(CODED ? c & 1 : c) * CH]);
         };
@@ -875,14 +902,44 @@ __global__ void __launch_bounds__((TreeCfg<KIND, D, PAIR>::THREADS), 1)
         if constexpr (CODED) {
           const int ss = (g + j) % C::NS;
           if (!(ok = mbar_wait_warp<true>(&sc_full[ss], ((g + j) / C::NS) & 1, SITE_TR_SM_SC))) break;
-          tmem_ld16(tS, chunk(0));
+          uint32_t(&h0)[32] = *reinterpret_cast<uint32_t(*)[32]>(&sr[0]);
+          uint32_t(&h1)[32] = *reinterpret_cast<uint32_t(*)[32]>(&sr[32]);
           sc = smem_u32(smem + C::OFF_SC) + ss * C::SC_BYTES;
-          auto find_max = [&](auto masked) {
-#pragma unroll 2
+          bool by_column = edge;
+          if (!edge) {
+            // The largest bare product times the largest (a negative one: the smallest) K scale, plus the largest
+            // log2 |V scale|, bounds the largest sum from above, and from no further than that product times the
+            // K scales' range plus the logarithms' range.  Any reference within a few powers of two of the
+            // maximum serves; columns are looked at one by one only where it is not.
+#pragma unroll 1
+            for (int h = 0; h < 2; ++h) {
+              tmem_ld32(tS + h * 64, h0);
+              tmem_ld32(tS + h * 64 + 32, h1);
+              tmem_wait_ld_regs(h0);
+              tmem_wait_ld_regs(h1);
+#pragma unroll
+              for (int i = 0; i < 64; i += 8) {
+                mx0 = max3(mx0, __uint_as_float(sr[i]), __uint_as_float(sr[i + 1]));
+                mx1 = max3(mx1, __uint_as_float(sr[i + 2]), __uint_as_float(sr[i + 3]));
+                mx2 = max3(mx2, __uint_as_float(sr[i + 4]), __uint_as_float(sr[i + 5]));
+                mx3 = max3(mx3, __uint_as_float(sr[i + 6]), __uint_as_float(sr[i + 7]));
+              }
+            }
+            const float4 ha = lds_f4(sc + 1536), hb = lds_f4(sc + 1552);
+            const float k_max = fmaxf(ha.x, hb.x), k_min = fminf(ha.y, hb.y);
+            const float g_max = fmaxf(ha.z, hb.z), g_min = fminf(ha.w, hb.w);
+            const float top = fmaxf(fmaxf(mx0, mx1), fmaxf(mx2, mx3));
+            mx0 = fmaf(top, top >= 0.f ? k_max : k_min, g_max);
+            mx1 = mx2 = mx3 = -INFINITY;
+            by_column = !__all_sync(0xffffffffu, fmaf(fabsf(top), k_max - k_min, g_max - g_min) <= 8.f);
+          }
+          if (by_column) {
+            mx0 = -INFINITY;
+#pragma unroll 1
             for (int c = 0; c < 8; ++c) {
-              uint32_t(&x)[CH] = chunk(c);
+              uint32_t(&x)[CH] = chunk(0);
+              tmem_ld16(tS + c * CH, x);
               tmem_wait_ld_regs(x);
-              tmem_ld16(tS + ((c + 1) & 7) * CH, chunk(c + 1));  // after the last, chunk 0 again for the weights
 #pragma unroll
               for (int i = 0; i < CH; i += 4) {
                 const float4 k4 = lds_f4(sc + (c * CH + i) * 4), g4 = lds_f4(sc + 1024 + (c * CH + i) * 4);
@@ -895,18 +952,15 @@ __global__ void __launch_bounds__((TreeCfg<KIND, D, PAIR>::THREADS), 1)
                 x[i + 2] = __float_as_uint(b2.x);
                 x[i + 3] = __float_as_uint(b2.y);
               }
-              if (masked.value) mask_chunk(c, x);
+              if (edge) mask_chunk(c, x);
 #pragma unroll
-              for (int i = 0; i < CH; i += 8) {
+              for (int i = 0; i < CH; i += 4) {
                 mx0 = max3(mx0, __uint_as_float(x[i]), __uint_as_float(x[i + 1]));
                 mx1 = max3(mx1, __uint_as_float(x[i + 2]), __uint_as_float(x[i + 3]));
-                mx2 = max3(mx2, __uint_as_float(x[i + 4]), __uint_as_float(x[i + 5]));
-                mx3 = max3(mx3, __uint_as_float(x[i + 6]), __uint_as_float(x[i + 7]));
               }
             }
-          };
-          if (edge) find_max(std::true_type{});
-          else find_max(std::false_type{});
+          }
+          tmem_ld16(tS, chunk(0));  // for the weights
         } else {
 #pragma unroll
           for (int c = 0; c < 4; ++c) tmem_ld32(tS + c * 32, chunk(c));
