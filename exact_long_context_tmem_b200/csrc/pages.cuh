@@ -51,36 +51,56 @@ __device__ __forceinline__ void copy_items(const CacheBufs& c, long long n_items
   const long long units = n_items * c.n_layers * per;
   long long u = blockIdx.x;
   if (u >= units) return;
+  // The CTA's next segments, one found by each thread: what item() costs (a search in the bitmap of live
+  // pages, for one) is paid side by side, not in front of every load.
+  __shared__ const char* seg_from[kCopyThreads];
+  __shared__ char* seg_to[kCopyThreads];
+  __shared__ int seg_left[kCopyThreads];  // bytes, negative: moved a word at a time
+  int at = 0, known = 0;
   const char* from = nullptr;  // the rest of the current segment
   char* to = nullptr;
-  long long left = 0;
+  int left = 0;
   bool wide = true;
+  auto find = [&](long long v) {
+    int seg, s = 0, src, dst, n_tok, layer, i;
+    if (units <= 0xffffffffLL) {
+      const unsigned r = (unsigned)v / (unsigned)per;
+      seg = (int)((unsigned)v - r * (unsigned)per);
+      i = (int)(r / (unsigned)c.n_layers);
+      layer = (int)(r - (unsigned)i * (unsigned)c.n_layers);
+    } else {
+      seg = (int)(v % per);
+      layer = (int)(v / per % c.n_layers);
+      i = (int)(v / per / c.n_layers);
+    }
+    item(i, src, dst, n_tok);
+    while (s + 1 < c.n && seg >= seg0[s + 1]) ++s;
+    const long long page = (long long)c.page_size * c.tok[s], off = (seg - seg0[s]) * seg_bytes;
+    seg_from[threadIdx.x] = c.p[s] + layer * c.layer[s] + src * page + off;
+    seg_to[threadIdx.x] = c.p[s] + layer * c.layer[s] + dst * page + off;
+    const int n = src == dst ? 0 : (int)max(0LL, min(seg_bytes, (long long)n_tok * c.tok[s] - off));
+    seg_left[threadIdx.x] = c.vec[s] == 16 ? n : -n;
+  };
   auto next = [&](Chunk& x) -> bool {
     while (left <= 0) {
-      if (u >= units) return false;
-      int seg, s = 0, src, dst, n_tok, layer, i;
-      if (units <= 0xffffffffLL) {
-        const unsigned r = (unsigned)u / (unsigned)per;
-        seg = (int)((unsigned)u - r * (unsigned)per);
-        i = (int)(r / (unsigned)c.n_layers);
-        layer = (int)(r - (unsigned)i * (unsigned)c.n_layers);
-      } else {
-        seg = (int)(u % per);
-        layer = (int)(u / per % c.n_layers);
-        i = (int)(u / per / c.n_layers);
+      if (at == known) {
+        if (u >= units) return false;
+        __syncthreads();
+        known = (int)min((long long)kCopyThreads, (units - u + gridDim.x - 1) / gridDim.x);
+        if ((int)threadIdx.x < known) find(u + (long long)threadIdx.x * gridDim.x);
+        u += (long long)known * gridDim.x;
+        at = 0;
+        __syncthreads();
       }
-      item(i, src, dst, n_tok);
-      while (s + 1 < c.n && seg >= seg0[s + 1]) ++s;
-      const long long page = (long long)c.page_size * c.tok[s], off = (seg - seg0[s]) * seg_bytes;
-      from = c.p[s] + layer * c.layer[s] + src * page + off;
-      to = c.p[s] + layer * c.layer[s] + dst * page + off;
-      left = src == dst ? 0 : min(seg_bytes, (long long)n_tok * c.tok[s] - off);
-      wide = c.vec[s] == 16;
-      u += gridDim.x;
+      from = seg_from[at];
+      to = seg_to[at];
+      left = abs(seg_left[at]);
+      wide = seg_left[at] >= 0;
+      ++at;
     }
     x.from = from;
     x.to = to;
-    x.bytes = (int)min(left, (long long)kChunkBytes);
+    x.bytes = min(left, kChunkBytes);
     x.wide = wide;
     from += kChunkBytes;
     to += kChunkBytes;
