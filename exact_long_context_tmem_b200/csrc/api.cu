@@ -116,6 +116,22 @@ static attn_status_t ensure_smem(K kernel, int bytes, std::atomic<uint64_t>& don
   return ATTN_OK;
 }
 
+// Launches a kernel whose CTAs may start while the kernel before it in the stream still runs; it waits for that
+// one with grid_dependency_wait before it reads anything.
+template <typename K, typename P, typename... A>
+static cudaError_t launch_dependent(K kernel, unsigned grid, unsigned threads, cudaStream_t stream, const P& p, A... rest) {
+  cudaLaunchAttribute attr{};
+  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr.val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3(grid);
+  cfg.blockDim = dim3(threads);
+  cfg.stream = stream;
+  cfg.attrs = &attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kernel, p, rest...);
+}
+
 static bool dims_ok(const attn_dims_t& d) {
   return d.B >= 0 && d.Hq > 0 && d.Hkv > 0 && d.Hq % d.Hkv == 0 && d.D > 0 && std::isfinite(d.scale) &&
          d.scale > 0.f;
@@ -497,8 +513,7 @@ static attn_status_t launch_tree(const void* q, const void* k, const void* v, co
     if (st != ATTN_OK) return st;
   }
   const long long rows = (long long)d.B * p.n_q * d.Hq;
-  tree_join_kernel<D><<<(unsigned)((rows + 7) / 8), 256, 0, stream>>>(p, t.rows, t.pair ? 2 : 1);
-  ATTN_CUDA(cudaGetLastError());
+  ATTN_CUDA(launch_dependent(tree_join_kernel<D>, (unsigned)((rows + 7) / 8), 256, stream, p, t.rows, t.pair ? 2 : 1));
   return ATTN_OK;
 }
 
@@ -1059,8 +1074,7 @@ attn_status_t attn_pages_fork(void* k, void* v, float* k_scale, float* v_scale, 
   if (n_children == 0) return ATTN_OK;
   const long long units = std::max<long long>((long long)n_children * n_layers * p.c.chunk0[p.c.n],
                                               ((long long)n_children * max_pages + kCopyThreads - 1) / kCopyThreads);
-  pages_fork_apply_kernel<<<copy_grid(units), kCopyThreads, 0, cs>>>(p);
-  ATTN_CUDA(cudaGetLastError());
+  ATTN_CUDA(launch_dependent(pages_fork_apply_kernel, (unsigned)copy_grid(units), kCopyThreads, cs, p));
   return ATTN_OK;
 }
 

@@ -511,6 +511,7 @@ __global__ void __launch_bounds__(kForkThreads) pages_fork_plan_kernel(const For
   __shared__ int bad, n_copies;
   const int N = p.c.num_pages, tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int page = p.c.page_size;
+  grid_launch_dependents();  // pages_fork_apply_kernel's CTAs wait on the other processors
   int* cnt = SMEM ? fork_smem : p.count;
   int* claim = SMEM ? fork_smem + N : p.claim;
   if (tid == 0) bad = n_copies = 0;
@@ -630,6 +631,7 @@ __global__ void __launch_bounds__(kForkThreads) pages_fork_plan_kernel(const For
 
 // The new table's rows and the kept parts of cut pages, over the whole GPU.
 __global__ void __launch_bounds__(kCopyThreads) pages_fork_apply_kernel(const ForkParams p) {
+  grid_dependency_wait();
   const bool fail = p.head[1];
   const int n_copies = p.head[0];
   const long long entries = (long long)p.n_child * p.max_pages;

@@ -152,6 +152,13 @@ __device__ __forceinline__ void named_barrier_sync(uint32_t id, uint32_t nthread
   asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(nthreads) : "memory");
 }
 
+// ---------------------------------------------------------------- dependent launches
+
+// In a kernel launched as the dependent of another (launch_dependent on the host): waits for that one to have
+// finished, its writes visible.  In the other: lets the dependent start its CTAs where there is room.
+__device__ __forceinline__ void grid_dependency_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+__device__ __forceinline__ void grid_launch_dependents() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
+
 // ---------------------------------------------------------------- TMA (no multicast)
 
 __device__ __forceinline__ void tma_prefetch_desc(const CUtensorMap* map) {

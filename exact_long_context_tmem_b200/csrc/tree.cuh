@@ -385,6 +385,7 @@ __global__ void __launch_bounds__((TreeCfg<KIND, D, PAIR>::THREADS), 1)
   const int warp = threadIdx.x >> 5;
   const int lane = threadIdx.x & 31;
   const int rb = (int)blockIdx.x % p.n_rb;
+  grid_launch_dependents();  // tree_join's CTAs find room as this kernel's leave
 
   if (threadIdx.x == 0) {
     mbar_init(q_full, CODED ? 4 : 1);
@@ -1219,6 +1220,7 @@ __global__ void __launch_bounds__(256) tree_join_kernel(const TreeParams p, int 
   constexpr int V = D / 32;
   const long long row = (long long)blockIdx.x * 8 + (threadIdx.x >> 5);
   const int lane = threadIdx.x & 31;
+  grid_dependency_wait();
   if (row >= (long long)p.B * p.n_q * p.Hq) return;
   const int h = (int)(row % p.Hq);
   const long long bi = row / p.Hq;
