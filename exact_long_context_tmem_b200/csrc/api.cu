@@ -119,12 +119,12 @@ static attn_status_t ensure_smem(K kernel, int bytes, std::atomic<uint64_t>& don
 // Launches a kernel whose CTAs may start while the kernel before it in the stream still runs; it waits for that
 // one with grid_dependency_wait before it reads anything.
 template <typename K, typename P, typename... A>
-static cudaError_t launch_dependent(K kernel, unsigned grid, unsigned threads, cudaStream_t stream, const P& p, A... rest) {
+static cudaError_t launch_dependent(K kernel, dim3 grid, unsigned threads, cudaStream_t stream, const P& p, A... rest) {
   cudaLaunchAttribute attr{};
   attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr.val.programmaticStreamSerializationAllowed = 1;
   cudaLaunchConfig_t cfg{};
-  cfg.gridDim = dim3(grid);
+  cfg.gridDim = grid;
   cfg.blockDim = dim3(threads);
   cfg.stream = stream;
   cfg.attrs = &attr;
@@ -468,7 +468,7 @@ static TreePlan tree_plan(const attn_dims_t& d, int Tmax, int n_q) {
   t.n_rb = (n_q + t.tps * slots - 1) / (t.tps * slots);
   t.rows = 128 * slots;
   const long long tiles = (long long)d.B * d.Hkv * (((long long)Tmax + 127) / 128);
-  t.n_groups = (int)std::max(1LL, std::min<long long>(sm_count() / t.n_rb, tiles));
+  t.n_groups = (int)std::max(1LL, std::min<long long>(std::min(sm_count(), kTreeMaxRanges) / t.n_rb, tiles));
   return t;
 }
 
@@ -512,8 +512,12 @@ static attn_status_t launch_tree(const void* q, const void* k, const void* v, co
                 : launch_tree_inst<KIND, D, false>(mq, mk, mv, p, stream);
     if (st != ATTN_OK) return st;
   }
-  const long long rows = (long long)d.B * p.n_q * d.Hq;
-  ATTN_CUDA(launch_dependent(tree_join_kernel<D>, (unsigned)((rows + 7) / 8), 256, stream, p, t.rows, t.pair ? 2 : 1));
+  const long long blocks = (long long)d.B * d.Hkv * t.n_rb * (t.rows / 32);
+  // Few rows: two columns a warp, so that there are CTAs enough to wait for memory side by side (32 rows of 8
+  // heads, 16 partials each: 25.6 us with eight columns, JOIN_FEW with two; 16 x 8 items of 64 rows: JOIN_MANY).
+  const int few = blocks < sm_count();
+  auto join = few ? tree_join_kernel<D, 2> : tree_join_kernel<D, 8>;
+  ATTN_CUDA(launch_dependent(join, dim3((unsigned)blocks, few ? D / 16 : D / 64), 256, stream, p, t.rows, t.pair ? 2 : 1));
   return ATTN_OK;
 }
 
@@ -532,8 +536,8 @@ static attn_status_t tree_call(const void* q, const void* k, const void* v, attn
   if (quant && (!aligned4(ks) || !aligned4(vs))) return ATTN_ERR_INVALID_ARG;
   const int G = d.Hq / d.Hkv;
   if (n_q > 64 || G > 128 || (d.D != 128 && (quant || d.D != 64))) return ATTN_ERR_UNSUPPORTED;
-  // Tiles, and rows of the join in blocks of 8, are int-indexed.
-  if (Tmax > 0x7fffff00 || (long long)d.B * d.Hkv > 0x7fffffffLL ||
+  // Tiles and the join's blocks (at most 8 * 32 an item) are int-indexed.
+  if (Tmax > 0x7fffff00 || (long long)d.B * d.Hkv > 0x7fffffffLL / 256 ||
       (long long)d.B * d.Hkv * (((long long)Tmax + 127) / 128) > 0x7fffffffLL ||
       (long long)d.B * d.Hq * n_q > 0x7fffffffLL)
     return ATTN_ERR_UNSUPPORTED;
@@ -1074,7 +1078,7 @@ attn_status_t attn_pages_fork(void* k, void* v, float* k_scale, float* v_scale, 
   if (n_children == 0) return ATTN_OK;
   const long long units = std::max<long long>((long long)n_children * n_layers * p.c.chunk0[p.c.n],
                                               ((long long)n_children * max_pages + kCopyThreads - 1) / kCopyThreads);
-  ATTN_CUDA(launch_dependent(pages_fork_apply_kernel, (unsigned)copy_grid(units), kCopyThreads, cs, p));
+  ATTN_CUDA(launch_dependent(pages_fork_apply_kernel, dim3((unsigned)copy_grid(units)), kCopyThreads, cs, p));
   return ATTN_OK;
 }
 

@@ -57,11 +57,14 @@ struct TreeParams {
   const float* v_scale;
   const int* page_table;    // [B, max_pages] or null (one page of Tmax tokens per sequence)
   int max_pages, page_size, num_pages;
-  float* part_o;            // [n_groups * n_rb * 2, rows, D] normalised partials
+  float* part_o;            // [n_groups * n_rb * 2, D, rows] normalised partials
   float* part_lse;          // [n_groups * n_rb * 2, rows] their log2-domain log-sum-exp
   __nv_bfloat16* o;         // [B, n_q, Hq, D]
   float* lse;               // [B, n_q, Hq] or null
 };
+
+// Ranges an item can be cut into: the launch has one CTA per processor, of which there are fewer.
+static constexpr int kTreeMaxRanges = 256;
 
 enum TreeKv { TREE_BF16 = 0, TREE_FP8 = 1, TREE_INT8 = 2, TREE_INT4 = 3 };
 
@@ -76,7 +79,8 @@ __device__ __forceinline__ int tree_qlen(const TreeParams& p, int b) {
 }
 // Key tiles of one KV head of sequence b (none when it drafts nothing).
 __device__ __forceinline__ int tree_tiles(const TreeParams& p, int b) {
-  return tree_qlen(p, b) > 0 ? (tree_len(p, b) + 127) >> 7 : 0;
+  const int qn = tree_qlen(p, b), n = (tree_len(p, b) + 127) >> 7;  // two loads at once, not one after the other
+  return qn > 0 ? n : 0;
 }
 
 // Pool page of token tok of sequence b, -1 (never dereferenced: TMA fills zeros, scales read as 0) for a
@@ -835,7 +839,6 @@ __global__ void __launch_bounds__((TreeCfg<KIND, D, PAIR>::THREADS), 1)
     const int tok_i = (rb * C::NQ + (PAIR ? slot : 0)) * p.tps + r / p.G;  // this row's drafted token
     const int head_g = r % p.G;
     const bool row_used = r < p.tps * p.G && tok_i < p.n_q;
-    const bool warp_used = __any_sync(0xffffffffu, row_used);  // else its rows of S, P and O are nobody's
     int cs = 0, g = 0, qi = 0, ub = 0;  // tiles of this slot, tiles of the CTA, pieces, units before this piece
     bool ok = true;
     // The walk and its piece are kept in shared memory, a copy per warp: between pieces they are dead weight,
@@ -865,25 +868,23 @@ __global__ void __launch_bounds__((TreeCfg<KIND, D, PAIR>::THREADS), 1)
         return (unsigned long long)__ldg(p.mask + (long long)it.b * p.n_q + tok_i) & tree_low_bits(it.qn);
       };
       float m_used = -INFINITY, l = 0.f;
-      if (CODED && !warp_used) {  // the tiles are only handed on
-        for (int j = PAIR ? 0 : slot; j < n && ok; j += PAIR ? 1 : 2) {
-          const int ss = (g + j) % (CODED ? C::NS : 1);
-          ok = mbar_wait_warp<true>(&s_full[slot], cs & 1, SITE_TR_SM_S) &&
-               mbar_wait_warp<true>(&sc_full[ss], ((g + j) / (CODED ? C::NS : 1)) & 1, SITE_TR_SM_SC);
-          if (ok && lane == 0) {
-            mbar_arrive(&p_full[slot]);
-            mbar_arrive(&sc_empty[ss]);
-          }
-          ++cs;
-        }
-        if (!ok) break;
-      }
-      for (int j = PAIR ? 0 : slot; j < n && (!CODED || warp_used); j += PAIR ? 1 : 2) {
+      const bool piece_used = __any_sync(0xffffffffu, row_ok);  // else this warp's rows of S, P and O are nobody's
+      for (int j = PAIR ? 0 : slot; j < n; j += PAIR ? 1 : 2) {
         // tcgen05.ld/st are warp-collective: every lane takes the same branch around them.
         if (!(ok = mbar_wait_warp<true>(&s_full[slot], cs & 1, SITE_TR_SM_S))) break;
         tc_fence_after();
         const int kv0 = (t0 + j) * 128;
         const bool edge = kv0 + 128 > base;
+        if (!piece_used && (CODED || !edge || (PAIR && slot == 1))) {  // the tile is only handed on
+          if constexpr (CODED) {
+            const int ss = (g + j) % C::NS;
+            if (!(ok = mbar_wait_warp<true>(&sc_full[ss], ((g + j) / C::NS) & 1, SITE_TR_SM_SC))) break;
+            if (lane == 0) mbar_arrive(&sc_empty[ss]);
+          }
+          if (lane == 0) mbar_arrive(&p_full[slot]);
+          ++cs;
+          continue;
+        }
         // bf16: sr holds the row's 128 scores, read as four chunks of 32.  Coded caches: half of them for the
         // maximum, then two chunks of 16 in turn for the weights; longer loop bodies, of which there are several
         // kinds in flight at once, run out of the instruction cache.
@@ -1131,12 +1132,14 @@ __global__ void __launch_bounds__((TreeCfg<KIND, D, PAIR>::THREADS), 1)
       tc_fence_after();
       const bool fix = *reinterpret_cast<volatile int*>(odd_piece + (qi & 7)) == qi + 1;
       const long long orow = ((long long)it.b * p.n_q + tok_i) * p.Hq + (long long)it.kvh * p.G + head_g;
-      const long long prow = ((long long)blockIdx.x * 2 + it.which) * C::ROWS + (PAIR ? slot * 128 : 0) + r;
+      const long long part = (long long)blockIdx.x * 2 + it.which;
+      const int prow = (PAIR ? slot * 128 : 0) + r;
       // PAIR: each slot stores its rows' D columns; halves: each slot stores half the columns of every row.
       constexpr int NCH = PAIR ? D / 32 : D / 64;
       const int ch0 = PAIR ? 0 : slot * NCH;
+      if (!piece_used && lane == 0) mbar_arrive(o_empty);
 #pragma unroll 1
-      for (int c = ch0; c < ch0 + NCH; ++c) {
+      for (int c = ch0; c < ch0 + NCH && piece_used; ++c) {
         uint32_t ov[32];
         tmem_ld32(tO + c * 32, ov);
         tmem_wait_ld_regs(ov);
@@ -1189,15 +1192,16 @@ __global__ void __launch_bounds__((TreeCfg<KIND, D, PAIR>::THREADS), 1)
               dst[i] = x;
             }
           } else {
-            float4* dst = reinterpret_cast<float4*>(p.part_o + prow * D + c * 32);
+            // Column by column: 32 rows' neighbouring floats a store (row by row, 16 bytes of 32 rows each, the stores
+            // took half of the 12,000 cycles of a piece's epilogue).
+            float* dst = p.part_o + (part * D + c * 32) * C::ROWS + prow;
 #pragma unroll
-            for (int i = 0; i < 8; ++i)
-              dst[i] = make_float4(out[4 * i], out[4 * i + 1], out[4 * i + 2], out[4 * i + 3]);
+            for (int i = 0; i < 32; ++i) dst[i * C::ROWS] = out[i];
           }
         }
       }
       if (row_ok && (PAIR || slot == 0)) {
-        if (!it.whole) p.part_lse[prow] = lse2;
+        if (!it.whole) p.part_lse[part * C::ROWS + prow] = lse2;
         else if (p.lse) p.lse[orow] = lse2 * 0.69314718055994531f;
       }
       g += n;
@@ -1213,77 +1217,89 @@ __global__ void __launch_bounds__((TreeCfg<KIND, D, PAIR>::THREADS), 1)
   }
 }
 
-// Joins the partials of items that several CTAs shared, and writes the rows no tile belongs to.
-// One warp per row (sequence b, token i, head h); a row whose item one CTA finished is left alone.
-template <int D>
+// Joins the partials of items that several CTAs shared, and writes the rows no tile belongs to.  A block takes 32
+// neighbouring rows of a row block (sequence b, KV head) and 8 NC of their columns: a lane per row, NC
+// columns per warp, so that partials are read a line at a time.  Rows that one CTA finished are left alone.
+template <int D, int NC>
 __global__ void __launch_bounds__(256) tree_join_kernel(const TreeParams p, int rows_per_part, int slots) {
-  constexpr int V = D / 32;
-  const long long row = (long long)blockIdx.x * 8 + (threadIdx.x >> 5);
-  const int lane = threadIdx.x & 31;
+  __shared__ float weight[kTreeMaxRanges][32];  // of each partial, row by row
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, c0 = ((int)blockIdx.y * 8 + warp) * NC;
   grid_dependency_wait();
-  if (row >= (long long)p.B * p.n_q * p.Hq) return;
-  const int h = (int)(row % p.Hq);
-  const long long bi = row / p.Hq;
-  const int i = (int)(bi % p.n_q), b = (int)(bi / p.n_q);
-  const int kvh = h / p.G, hg = h % p.G;
+  int x = (int)blockIdx.x;
+  const int prow = x % (rows_per_part / 32) * 32 + lane;
+  x /= rows_per_part / 32;
+  const int rb = x % p.n_rb;
+  x /= p.n_rb;
+  const int kvh = x % p.Hkv, b = x / p.Hkv;
+  const int r = prow & 127, i = (rb * slots + (prow >> 7)) * p.tps + r / p.G;
+  const bool used = r < p.tps * p.G && i < p.n_q;
+  if (!__any_sync(0xffffffffu, used)) return;
   int total = 0, before = 0;
-  for (int x = lane; x < p.B; x += 32) {
-    const int n = tree_tiles(p, x);
+  for (int y = lane; y < p.B; y += 32) {
+    const int n = tree_tiles(p, y);
     total += n;
-    if (x < b) before += n;
+    if (y < b) before += n;
   }
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) {
     total += __shfl_xor_sync(0xffffffffu, total, o);
     before += __shfl_xor_sync(0xffffffffu, before, o);
   }
-  const int tiles = tree_tiles(p, b);
-  float acc[V];
+  const int tiles = tree_tiles(p, b), qn = tree_qlen(p, b);
+  const bool wanted = used && i < qn && tiles > 0;
+  float acc[NC];
 #pragma unroll
-  for (int k = 0; k < V; ++k) acc[k] = 0.f;
+  for (int k = 0; k < NC; ++k) acc[k] = 0.f;
   float out = -INFINITY;
-  if (i < tree_qlen(p, b) && tiles > 0) {
+  if (tiles > 0) {  // the same for the whole block
     const int W = total * p.Hkv, ng = min(p.n_groups, W);
     const int a = before * p.Hkv + kvh * tiles;
     const int g0 = (int)(((long long)(a + 1) * ng - 1) / W), g1 = (int)(((long long)(a + tiles) * ng - 1) / W);
-    if (g0 == g1) return;  // finished by its CTA
-    const int s = i / p.tps, rb = s / slots;
-    const int prow = (s % slots) * 128 + (i % p.tps) * p.G + hg;
-    auto part = [&](int g) -> long long {
-      const int which = g == g0 && a > tree_range(g0, W, ng) ? 1 : 0;
-      return (((long long)g * p.n_rb + rb) * 2 + which) * rows_per_part + prow;
-    };
-    float mx = -INFINITY;
-    bool nan = false;
-    for (int g = g0 + lane; g <= g1; g += 32) {
-      const float x = p.part_lse[part(g)];
-      nan |= x != x;
-      mx = fmaxf(mx, x);
-    }
-    mx = warp_max(mx);
-    if (__any_sync(0xffffffffu, nan)) mx = __int_as_float(0x7fc00000);
-    if (mx != -INFINITY) {
-      float sum = 0.f;
-      for (int g = g0 + lane; g <= g1; g += 32) sum += ex2_approx(p.part_lse[part(g)] - mx);
-      sum = warp_sum(sum);
-      out = (mx + log2f(sum)) * 0.69314718055994531f;
-      const float inv = 1.f / sum;
-#pragma unroll 4
-      for (int g = g0; g <= g1; ++g) {
-        const long long q = part(g);
-        const float lq = p.part_lse[q];
-        if (lq == -INFINITY) continue;
-        const float wgt = ex2_approx(lq - mx) * inv;
-        const float* src = p.part_o + q * D + lane * V;
+    if (g0 == g1) {  // finished by its CTA
+      if (wanted) return;
+    } else {
+      const int n = g1 - g0 + 1;
+      const bool inside = a > tree_range(g0, W, ng);  // the item begins within its first range
+      auto part = [&](int k) -> long long {
+        return ((long long)(g0 + k) * p.n_rb + rb) * 2 + (k == 0 && inside ? 1 : 0);
+      };
+      for (int k = warp; k < n; k += 8)
+        weight[k][lane] = wanted ? p.part_lse[part(k) * rows_per_part + prow] : -INFINITY;
+      __syncthreads();
+      float mx = -INFINITY, sum = 0.f;
+      bool nan = false;
+      for (int k = 0; k < n; ++k) {
+        const float y = weight[k][lane];
+        nan |= y != y;
+        mx = fmaxf(mx, y);
+      }
+      if (nan) mx = __int_as_float(0x7fc00000);
+      if (mx != -INFINITY) {
+        const float* src = p.part_o + (long long)c0 * rows_per_part + prow;
+#pragma unroll(64 / NC)
+        for (int k = 0; k < n; ++k) {
+          const float w = ex2_approx(weight[k][lane] - mx);
+          sum += w;
+          const float* s = src + part(k) * D * rows_per_part;
 #pragma unroll
-        for (int k = 0; k < V; ++k) acc[k] = fmaf(wgt, src[k], acc[k]);
+          for (int c = 0; c < NC; ++c) {
+            const float y = s[c * rows_per_part];
+            acc[c] = w == 0.f ? acc[c] : fmaf(w, y, acc[c]);  // a part that saw nothing holds anything
+          }
+        }
+        out = (mx + log2f(sum)) * 0.69314718055994531f;
+        const float inv = 1.f / sum;
+#pragma unroll
+        for (int c = 0; c < NC; ++c) acc[c] *= inv;
       }
     }
   }
-  uint32_t* dst = reinterpret_cast<uint32_t*>(p.o + row * D + lane * V);
+  if (!used) return;
+  const long long row = ((long long)b * p.n_q + i) * p.Hq + (long long)kvh * p.G + r % p.G;
+  uint32_t* dst = reinterpret_cast<uint32_t*>(p.o + row * D + c0);
 #pragma unroll
-  for (int k = 0; k < V / 2; ++k) dst[k] = pack_bf16x2(acc[2 * k], acc[2 * k + 1]);
-  if (p.lse && lane == 0) p.lse[row] = out;
+  for (int k = 0; k < NC / 2; ++k) dst[k] = pack_bf16x2(acc[2 * k], acc[2 * k + 1]);
+  if (p.lse && c0 == 0) p.lse[row] = out;
 }
 
 }  // namespace attn
