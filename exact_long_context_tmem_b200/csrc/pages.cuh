@@ -7,7 +7,7 @@
 // scales, each [layers, pages, page_size, tok_bytes].
 #pragma once
 
-#include "ptx.cuh"
+#include "device_ext.cuh"
 
 namespace attn {
 

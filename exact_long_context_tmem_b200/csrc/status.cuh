@@ -10,7 +10,6 @@ enum DeviceErrorCode : uint32_t {
   ATTN_DEV_OK = 0,
   ATTN_DEV_TIMEOUT = 1,  // a bounded wait ran out
   ATTN_DEV_BAD_PAGE = 2,  // a decode page-table entry outside [0, num_pages)
-  ATTN_DEV_BAD_INDEX = 3,  // an index or length among the arguments on the device is out of range
 };
 
 // Wait sites, recorded with the error so a timeout names the wait that gave up.
@@ -39,38 +38,15 @@ enum WaitSite : int {
   SITE_DC_MMA_S = 42,
   SITE_DC_SM_P = 43,
   SITE_DC_PAGE = 44,
-  SITE_TR_LOAD = 50,
-  SITE_TR_MMA_Q = 51,
-  SITE_TR_MMA_U = 52,
-  SITE_TR_MMA_P = 53,
-  SITE_TR_CONV = 54,
-  SITE_TR_SM_S = 55,
-  SITE_TR_SM_SC = 56,
-  SITE_TR_SM_V = 57,
-  SITE_TR_EPI = 58,
-  SITE_TR_DRAIN = 59,
-  SITE_TR_PAGE = 60,
-  SITE_TR_SCALE = 61,
-  SITE_ACCEPT = 70,
-  SITE_PAGES_COPY = 71,
-  SITE_PAGES_COMPACT = 72,
-  SITE_PAGES_FORK = 73,
 };
 
 // (code << 16) | site of the first error since the last reset; 0 when clean.
 __device__ uint32_t g_dev_status = 0;
-// The same for bad arguments met on the device.  A word of its own: waits give up when
-// g_dev_status is set, and an index that was skipped is no reason for other work to stop.
-__device__ uint32_t g_arg_status = 0;
 // Upper bound for any single mbarrier wait, in nanoseconds of %globaltimer.
 __device__ uint64_t g_wait_limit_ns = 2000000000ull;
 
 __device__ __forceinline__ void record_device_error(uint32_t code, int site) {
   atomicCAS(&g_dev_status, 0u, (code << 16) | (uint32_t)(site & 0xFFFF));
-}
-
-__device__ __forceinline__ void record_arg_error(uint32_t code, int site) {
-  atomicCAS(&g_arg_status, 0u, (code << 16) | (uint32_t)(site & 0xFFFF));
 }
 
 __device__ __forceinline__ bool device_error_set() {

@@ -39,7 +39,7 @@
 #include <type_traits>
 
 #include "decode_int.cuh"
-#include "ptx.cuh"
+#include "device_ext.cuh"
 
 namespace attn {
 
@@ -380,8 +380,8 @@ __global__ void __launch_bounds__((TreeCfg<KIND, D, PAIR>::THREADS), 1)
   uint64_t* drain = ml_empty + 1;
   uint32_t* tmem_holder = reinterpret_cast<uint32_t*>(drain + 1);
   int* walk0 = reinterpret_cast<int*>(tmem_holder + 1);   // [3]
-  // odd_piece[i & 7] = i + 1 when piece i holds a non-finite draft V.  Whoever finds one runs at most a
-  // ring of units ahead of the epilogue that asks (NU <= 6, two units or more a piece): eight entries.
+  // odd_piece[i & 7] = i + 1 when piece i holds a non-finite draft V.  Whoever finds one runs at most a ring ahead
+  // of the epilogue that asks (NU <= 6 units, two or more a piece; NS = 4 tiles of scales): eight entries.
   int* odd_piece = walk0 + 3;
   uint32_t* q_max = reinterpret_cast<uint32_t*>(odd_piece + 8);  // [4] largest |q| (bf16 bits) per converter warp
   float* q_down = reinterpret_cast<float*>(q_max + 4);  // what undoes the queries' power of two

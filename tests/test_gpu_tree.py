@@ -364,3 +364,69 @@ def test_queries_of_any_size(cuda_device, kind):
         d["k_scale"] *= 2.0**-60
     check(*tree(d, kind, cuda_device), d, kind)
     device_clean()
+
+
+@pytest.mark.parametrize("kind", ["bf16", "int8"])
+def test_more_drafts_than_tokens(cuda_device, kind):
+    """A length below the number of drafts: the cache holds the last of them only."""
+    q_lens = [9, 9, 9]
+    d = make(kind, 3, 9, 4, 2, [3, 1, 8], 128, seed=31)
+    mask = torch.full((3, 9), -1, dtype=torch.int64)
+    mask[0, 2] = (1 << 6) - 1  # none of the three that are there
+    o, lse = tree(d, kind, cuda_device, q_lens=q_lens, mask=mask)
+    check(o, lse, d, kind, q_lens=q_lens, mask=mask)
+    assert torch.isneginf(lse[0, 2]).all()
+    device_clean()
+
+
+def test_outputs_and_workspace_of_the_caller(cuda_device):
+    dev = cuda_device
+    d = make("fp8", 2, 20, 16, 4, [700, 333], 768, seed=40)
+    (k, v), sc = caches(d, "fp8", dev)
+    args = (d["q"].to(dev), k, v, d["kv_lens"].to(dev), d["mask"].to(dev))
+    want, wl = A.attn_decode_tree(*args, **sc)
+    need = A.attn_decode_tree_workspace_bytes(2, 16, 4, 128, 768, 20)
+    ws = torch.empty(need, dtype=torch.uint8, device=dev)
+    o = torch.full_like(want, math.nan)
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    got, none = A.attn_decode_tree(*args, **sc, o=o, ws=ws, want_lse=False, stream=s.cuda_stream)
+    torch.cuda.synchronize()
+    assert got is o and none is None and torch.equal(o, want)
+    lse = torch.empty_like(wl)
+    A.attn_decode_tree(*args, **sc, o=o, lse=lse, ws=ws)
+    assert torch.equal(lse, wl)
+    with pytest.raises(A.AttnError):
+        A.attn_decode_tree(*args, **sc, ws=ws[:-16])
+    with pytest.raises(ValueError):
+        A.attn_decode_tree(*args[:4], d["mask"].to(dev).int(), **sc)
+    with pytest.raises(ValueError):
+        A.attn_decode_tree(*args, **sc, q_lens=torch.ones(2, dtype=torch.int64, device=dev))
+    device_clean()
+
+
+def test_long_cache_past_32_bit_offsets(cuda_device):
+    """One sequence of more than 2^31 elements of K: the last tiles are read where they are."""
+    dev, T, n_q = cuda_device, 2**21 + 200, 5
+    k = torch.zeros(1, T, 8, 128, dtype=torch.bfloat16, device=dev)
+    v = torch.zeros_like(k)
+    g = torch.Generator().manual_seed(3)
+    k[0, -300:] = 3 * torch.randn(300, 8, 128, generator=g).to(torch.bfloat16).to(dev)
+    v[0, -300:] = torch.randn(300, 8, 128, generator=g).to(torch.bfloat16).to(dev)
+    q = (4 * torch.randn(1, n_q, 16, 128, generator=g)).to(torch.bfloat16)
+    mask = random_masks(np.random.default_rng(5), 1, n_q)
+    lens = torch.tensor([T], dtype=torch.int32)
+    o, lse = A.attn_decode_tree(q.to(dev), k, v, lens.to(dev), mask.to(dev))
+    # by hand: the zero keys have score 0 and value 0, so they only add their number to each sum
+    kt, vt = to_np(k[0, -300:]), to_np(v[0, -300:])
+    m = mask.numpy().view(np.uint64)[0]
+    for i in range(n_q):
+        see = np.array([t < 300 - n_q or bool(int(m[i]) >> (t - 300 + n_q) & 1) for t in range(300)])
+        for h in range(16):
+            s = to_np(q)[0, i, h] @ kt[see, h // 2].T / math.sqrt(128)
+            total = np.exp(s).sum() + (T - 300)
+            ref = np.exp(s) @ vt[see, h // 2] / total
+            size = np.exp(s) @ np.abs(vt[see, h // 2]) / total
+            assert (np.abs(to_np(o)[0, i, h] - ref) <= 2.0**-8 * np.abs(ref) + (2.0**-8 + 2.0**-11) * size).all()
+            assert abs(float(lse[0, i, h]) - math.log(total)) <= 2.0**-11 + 2.0**-20 * math.log(total)
+    device_clean()
