@@ -760,21 +760,25 @@ __global__ void __launch_bounds__((TreeCfg<KIND, D, PAIR>::THREADS), 1)
       // The piece's queries, bf16 -> f16 in place, times a power of two that takes the largest |q| to
       // [2^14, 2^15).  What falls below f16's normal range is then off by at most 2^-39 of the largest,
       // far less than fp32 accumulation loses on it.
-      auto convert_q = [&]() -> bool {
+      auto convert_q = [&](const TreePiece& it) -> bool {
         if (!mbar_wait_warp<true>(q_raw, qi & 1, SITE_TR_CONV)) return false;
-        constexpr int CHUNKS = C::NQ * C::TILE_BYTES / 16;
-        uint4* qs = reinterpret_cast<uint4*>(smem + C::OFF_Q);
-        const int rows = p.tps * p.G;  // the others are never written: what they hold is not looked at
+        // Only rows of drafts there are: nobody looks at the others, nor at what they turn into.
+        const uint32_t qs = smem_u32(smem + C::OFF_Q) + t * 16;
         uint32_t top = 0;
-        for (int i = t; i < CHUNKS; i += 128) {
-          if (((i >> 3) & 127) >= rows) continue;
-          const uint4 x = qs[i];
-          const uint32_t w[4] = {x.x, x.y, x.z, x.w};
+#pragma unroll 1
+        for (int x = 0; x < C::NQ * C::NBOX; ++x) {
+          const int chunks = min(max(it.qn - (rb * C::NQ + x / C::NBOX) * p.tps, 0), p.tps) * p.G * 8;
+          const uint32_t at = qs + x * C::BOX_BYTES;
+#pragma unroll 4
+          for (int i = t; i < chunks; i += 128) {
+            const uint4 v = lds_u4(at + (i - t) * 16);
+            const uint32_t w[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
-          for (int k = 0; k < 4; ++k) {
-            const uint32_t lo = w[k] & 0x7fffu, hi = (w[k] >> 16) & 0x7fffu;
-            if (lo < 0x7f80u) top = max(top, lo);
-            if (hi < 0x7f80u) top = max(top, hi);
+            for (int k = 0; k < 4; ++k) {
+              const uint32_t lo = w[k] & 0x7fffu, hi = (w[k] >> 16) & 0x7fffu;
+              if (lo < 0x7f80u) top = max(top, lo);
+              if (hi < 0x7f80u) top = max(top, hi);
+            }
           }
         }
         top = __reduce_max_sync(0xffffffffu, top);
@@ -784,22 +788,29 @@ __global__ void __launch_bounds__((TreeCfg<KIND, D, PAIR>::THREADS), 1)
         const int shift = min(14 + 127 - max((int)(top >> 7), 1), 127);
         const float up = __uint_as_float((uint32_t)(127 + shift) << 23);
         if (t == 0) *q_down = exp2f((float)-shift);
-        for (int i = t; i < CHUNKS; i += 128) {
-          if (((i >> 3) & 127) >= rows) continue;
-          const uint4 x = qs[i];
-          const uint32_t w[4] = {x.x, x.y, x.z, x.w};
-          float f[8];
+#pragma unroll 1
+        for (int x = 0; x < C::NQ * C::NBOX; ++x) {
+          const int chunks = min(max(it.qn - (rb * C::NQ + x / C::NBOX) * p.tps, 0), p.tps) * p.G * 8;
+          const uint32_t at = qs + x * C::BOX_BYTES;
+#pragma unroll 2
+          for (int i = t; i < chunks; i += 128) {
+            const uint4 v = lds_u4(at + (i - t) * 16);
+            const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+            float f[8];
 #pragma unroll
-          for (int k = 0; k < 4; ++k) {
-            f[2 * k] = __uint_as_float(w[k] << 16) * up;
-            f[2 * k + 1] = __uint_as_float(w[k] & 0xffff0000u) * up;
+            for (int k = 0; k < 4; ++k) {
+              f[2 * k] = __uint_as_float(w[k] << 16) * up;
+              f[2 * k + 1] = __uint_as_float(w[k] & 0xffff0000u) * up;
+            }
+            uint4 h;
+            if constexpr (KIND == TREE_INT4)
+              h = make_uint4(pack_f16x2(f[0], f[4]), pack_f16x2(f[1], f[5]), pack_f16x2(f[2], f[6]),
+                             pack_f16x2(f[3], f[7]));
+            else
+              h = make_uint4(pack_f16x2(f[0], f[1]), pack_f16x2(f[2], f[3]), pack_f16x2(f[4], f[5]),
+                             pack_f16x2(f[6], f[7]));
+            sts_u4(at + (i - t) * 16, h);
           }
-          if constexpr (KIND == TREE_INT4)
-            qs[i] = make_uint4(pack_f16x2(f[0], f[4]), pack_f16x2(f[1], f[5]), pack_f16x2(f[2], f[6]),
-                               pack_f16x2(f[3], f[7]));
-          else
-            qs[i] = make_uint4(pack_f16x2(f[0], f[1]), pack_f16x2(f[2], f[3]), pack_f16x2(f[4], f[5]),
-                               pack_f16x2(f[6], f[7]));
         }
         fence_proxy_async_smem();
         __syncwarp();
@@ -811,7 +822,7 @@ __global__ void __launch_bounds__((TreeCfg<KIND, D, PAIR>::THREADS), 1)
       w.init(p, walk0);
       while (ok && w.next(p, it)) {
         const int n = it.n;
-        ok = convert_q();
+        ok = convert_q(it);
         for (int x = 0; x < 2 * n && ok; ++x) {  // the units of the piece, in the order of tree_v_unit
           bool is_v;
           int j;
@@ -875,7 +886,7 @@ __global__ void __launch_bounds__((TreeCfg<KIND, D, PAIR>::THREADS), 1)
         tc_fence_after();
         const int kv0 = (t0 + j) * 128;
         const bool edge = kv0 + 128 > base;
-        if (!piece_used && (CODED || !edge || (PAIR && slot == 1))) {  // the tile is only handed on
+        if (CODED && !piece_used) {  // the tile is only handed on
           if constexpr (CODED) {
             const int ss = (g + j) % C::NS;
             if (!(ok = mbar_wait_warp<true>(&sc_full[ss], ((g + j) / C::NS) & 1, SITE_TR_SM_SC))) break;
@@ -1137,9 +1148,9 @@ __global__ void __launch_bounds__((TreeCfg<KIND, D, PAIR>::THREADS), 1)
       // PAIR: each slot stores its rows' D columns; halves: each slot stores half the columns of every row.
       constexpr int NCH = PAIR ? D / 32 : D / 64;
       const int ch0 = PAIR ? 0 : slot * NCH;
-      if (!piece_used && lane == 0) mbar_arrive(o_empty);
+      if (CODED && !piece_used && lane == 0) mbar_arrive(o_empty);
 #pragma unroll 1
-      for (int c = ch0; c < ch0 + NCH && piece_used; ++c) {
+      for (int c = ch0; c < ch0 + NCH && (piece_used || !CODED); ++c) {
         uint32_t ov[32];
         tmem_ld32(tO + c * 32, ov);
         tmem_wait_ld_regs(ov);
