@@ -1028,16 +1028,20 @@ __global__ void __launch_bounds__((TreeCfg<KIND, D, PAIR>::THREADS), 1)
 #pragma unroll 2
             for (int c = 0; c < 8; ++c) {
               uint32_t(&x)[CH] = chunk(c);
+              float4 k4[4], v4[4];  // asked for ahead of the waits that come before their use
+#pragma unroll
+              for (int i = 0; i < 4; ++i) k4[i] = lds_f4(sc + c * 64 + i * 16);
               tmem_wait_ld_regs(x);
               // P lands in columns 8 c .. 8 c + 7, all below the chunk that is still to be read.
               if (c < 7) tmem_ld16(tS + (c + 1) * CH, chunk(c + 1));
 #pragma unroll
+              for (int i = 0; i < 4; ++i) v4[i] = lds_f4(sc + 512 + c * 64 + i * 16);
+#pragma unroll
               for (int i = 0; i < CH; i += 4) {
-                const float4 k4 = lds_f4(sc + (c * CH + i) * 4);
                 const float2 a = fma2(make_float2(__uint_as_float(x[i]), __uint_as_float(x[i + 1])),
-                                      make_float2(k4.x, k4.y), nm2);
+                                      make_float2(k4[i / 4].x, k4[i / 4].y), nm2);
                 const float2 b2 = fma2(make_float2(__uint_as_float(x[i + 2]), __uint_as_float(x[i + 3])),
-                                       make_float2(k4.z, k4.w), nm2);
+                                       make_float2(k4[i / 4].z, k4[i / 4].w), nm2);
                 x[i] = __float_as_uint(a.x);
                 x[i + 1] = __float_as_uint(a.y);
                 x[i + 2] = __float_as_uint(b2.x);
@@ -1055,9 +1059,8 @@ __global__ void __launch_bounds__((TreeCfg<KIND, D, PAIR>::THREADS), 1)
                 add_sum(i + 1, e1);
                 // The weight times its V scale is rounded once, to f16 (at most 2^-11 of it, or 2^-25 of the row's
                 // largest such product).
-                const float4 v4 = lds_f4(sc + 512 + (c * CH + 2 * i) * 4);
-                e0 = mul2(e0, make_float2(v4.x, v4.y));
-                e1 = mul2(e1, make_float2(v4.z, v4.w));
+                e0 = mul2(e0, make_float2(v4[i / 2].x, v4[i / 2].y));
+                e1 = mul2(e1, make_float2(v4[i / 2].z, v4[i / 2].w));
                 pk[i] = pack_f16x2(e0.x, e0.y);
                 pk[i + 1] = pack_f16x2(e1.x, e1.y);
               }
