@@ -567,7 +567,7 @@ def attn_tree_accept(k, v, kv_lens, path, n_accepted, *, n_q: int | None = None,
     device = _one_device(k, v, kv_lens, path, n_accepted, q_lens,
                          page_table, k_scale, v_scale, kv_lens_out)
     layers, pages, page_size, Hkv, row = _cache(k, v, k_scale, v_scale)
-    B = kv_lens.shape[0]
+    B = kv_lens.numel()
     n_q = path.shape[-1] if n_q is None else int(n_q)
     _expect("kv_lens", kv_lens, torch.int32, (B,))
     _expect("path", path, torch.int32, (B, n_q))
@@ -578,7 +578,7 @@ def attn_tree_accept(k, v, kv_lens, path, n_accepted, *, n_q: int | None = None,
         raise ValueError(f"k/v: expected {B} sequences (the length of kv_lens), got {pages}")
     if page_table is not None and _table(page_table)[0] != B:
         raise ValueError(f"page_table: expected {B} rows, got {page_table.shape[0]}")
-    if kv_lens_out is not None and kv_lens_out.data_addr() == kv_lens.data_addr():
+    if kv_lens_out is not None and kv_lens_out.data_ptr() == kv_lens.data_ptr():
         raise ValueError("kv_lens_out: expected memory of its own, got kv_lens")
     with _On(device, stream) as st:
         if kv_lens_out is None:

@@ -91,6 +91,20 @@ def test_accept_one_layer_without_its_dimension(cuda_device):
     device_clean()
 
 
+def test_accept_writes_the_lengths_where_it_is_told(cuda_device):
+    dev = cuda_device
+    k, v, _, _ = make_cache("bf16", (1, 2, 64), 2, 1, dev)
+    lens, path, n = ints([64, 14], dev), ints([[1, 3, 0, 0], [2, 0, 0, 0]], dev), ints([2, 1], dev)
+    with pytest.raises(ValueError, match="kv_lens_out"):
+        A.attn_tree_accept(k[0], v[0], lens, path, n, kv_lens_out=lens)
+    with pytest.raises(ValueError, match="kv_lens"):
+        A.attn_tree_accept(k[0], v[0], lens[0], path[:1], n[:1])
+    room = ints([-7, -7, -7], dev)
+    out = A.attn_tree_accept(k[0], v[0], lens, path, n, kv_lens_out=room[:2])
+    assert out.data_ptr() == room.data_ptr() and room.tolist() == [62, 11, -7] and lens.tolist() == [64, 14]
+    device_clean()
+
+
 @pytest.mark.parametrize("bad", ["draft", "count", "length", "page", "negative"])
 def test_accept_leaves_a_bad_sequence_alone(cuda_device, bad):
     dev = cuda_device
