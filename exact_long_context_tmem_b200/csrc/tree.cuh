@@ -944,7 +944,8 @@ __global__ void __launch_bounds__((TreeCfg<KIND, D, PAIR>::THREADS), 1)
             const float top = fmaxf(fmaxf(mx0, mx1), fmaxf(mx2, mx3));
             mx0 = fmaf(top, top >= 0.f ? k_max : k_min, g_max);
             mx1 = mx2 = mx3 = -INFINITY;
-            by_column = !__all_sync(0xffffffffu, fmaf(fabsf(top), k_max - k_min, g_max - g_min) <= 8.f);
+            // Lanes without a row hold anything, and must not sway which way (and so which rounding) the others take.
+            by_column = !__all_sync(0xffffffffu, !row_ok || fmaf(fabsf(top), k_max - k_min, g_max - g_min) <= 8.f);
           }
           if (by_column) {
             mx0 = -INFINITY;

@@ -250,6 +250,26 @@ def test_many_sequences_share_ctas(cuda_device, kind, n_q, G):
     device_clean()
 
 
+@pytest.mark.parametrize("kind", list(KINDS))
+@pytest.mark.parametrize("n_q,G", [(40, 4), (64, 4), (60, 7), (16, 4), (17, 4), (21, 3), (64, 1), (1, 64), (1, 65)])
+def test_uneven_drafts_around_a_row_slot(cuda_device, kind, n_q, G):
+    """Sequences whose drafts fill one slot of rows, a part of it or more, one behind the other on a CTA."""
+    g = np.random.default_rng(n_q)
+    tps, B = min(128 // G, 64), 48
+    q_lens = [min(n_q, max(0, int(x))) for x in g.choice([0, 1, tps // 2, tps - 1, tps, tps + 1, 2 * tps, n_q], B)]
+    lens = [max(q, int(x)) for q, x in zip(q_lens, g.integers(1, 700, size=B))]
+    d = make(kind, B, n_q, 4 * G, 4, lens, 704, seed=n_q + G)
+    o, lse = tree(d, kind, cuda_device, q_lens=q_lens)
+    again = tree(d, kind, cuda_device, q_lens=q_lens)
+    assert torch.equal(o, again[0]) and torch.equal(lse, again[1])
+    pick = [0, 1, 2, 3, 20, 21, 46, 47]
+    sub = {x: (y[pick] if isinstance(y, torch.Tensor) else y) for x, y in d.items()}
+    check(o[pick], lse[pick], sub, kind, q_lens=[q_lens[b] for b in pick])
+    for b, n in enumerate(q_lens):
+        assert torch.isneginf(lse[b, n:]).all() and (o[b, n:] == 0).all()
+    device_clean()
+
+
 def test_bad_page_is_reported_and_stays_local(cuda_device):
     dev = cuda_device
     d = make("bf16", 2, 5, 8, 2, [500, 300], 512, seed=1)
