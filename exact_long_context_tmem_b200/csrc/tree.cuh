@@ -214,7 +214,7 @@ struct TreeCfg {
   static constexpr int OFF_ML = OFF_SC + NS * (1536 + 32);            // [2 slots][128] (max, sum) of the halves
   static constexpr int OFF_WALK = OFF_ML + (PAIR ? 0 : 2048);  // [8] walks, [8] pieces of the softmax warps
   static constexpr int OFF_BAR = OFF_WALK + 8 * (int)(sizeof(TreeWalk) + sizeof(TreePiece));
-  static constexpr int N_BARS = 3 + 2 * NU + 2 * NR + 2 * NS + 2 + 2 + 2 + 2 + 1;
+  static constexpr int N_BARS = 3 + 2 * NU + 2 * NR + 2 * NS + 2 + 2 + 2 + 2 + 1 + 1;
   static constexpr int SMEM_BYTES = OFF_BAR + N_BARS * 8 + 72 + 1024;  // + walk start, flags, alignment slack
   static constexpr int THREADS = CODED ? 512 : 384;
   // Register split: the softmax holds a row's 128 scores (bf16) or half of them (coded caches, of whose 512
@@ -378,7 +378,8 @@ __global__ void __launch_bounds__((TreeCfg<KIND, D, PAIR>::THREADS), 1)
   uint64_t* ml_full = o_empty + 1;      // the halves' (max, sum) are in shared memory (8 warps)
   uint64_t* ml_empty = ml_full + 1;     // ... and have been read
   uint64_t* drain = ml_empty + 1;
-  uint32_t* tmem_holder = reinterpret_cast<uint32_t*>(drain + 1);
+  uint64_t* q_meet = drain + 1;         // the converter warps' q_max are in shared memory
+  uint32_t* tmem_holder = reinterpret_cast<uint32_t*>(q_meet + 1);
   int* walk0 = reinterpret_cast<int*>(tmem_holder + 1);   // [3]
   // odd_piece[i & 7] = i + 1 when piece i holds a non-finite draft V.  Whoever finds one runs at most a ring ahead
   // of the epilogue that asks (NU <= 6 units, two or more a piece; NS = 4 tiles of scales): eight entries.
@@ -416,6 +417,7 @@ __global__ void __launch_bounds__((TreeCfg<KIND, D, PAIR>::THREADS), 1)
     mbar_init(ml_full, 8);
     mbar_init(ml_empty, 8);
     mbar_init(drain, 1);
+    mbar_init(q_meet, 4);
     for (int i = 0; i < 8; ++i) odd_piece[i] = 0;
     fence_barrier_init();
   }
@@ -782,8 +784,12 @@ __global__ void __launch_bounds__((TreeCfg<KIND, D, PAIR>::THREADS), 1)
           }
         }
         top = __reduce_max_sync(0xffffffffu, top);
-        if (lane == 0) q_max[cw] = top;
-        named_barrier_sync(1, 128);
+        if (lane == 0) {
+          q_max[cw] = top;
+          mbar_arrive(q_meet);
+        }
+        // Not a named barrier, whose wait has no limit should another warp have given up.
+        if (!mbar_wait_warp<true>(q_meet, qi & 1, SITE_TR_CONV)) return false;
         top = max(max(q_max[0], q_max[1]), max(q_max[2], q_max[3]));
         const int shift = min(14 + 127 - max((int)(top >> 7), 1), 127);
         const float up = __uint_as_float((uint32_t)(127 + shift) << 23);
