@@ -15,6 +15,8 @@
 //   !PAIR (n_q <= tps): the two slots hold the same rows and take alternate key tiles; their softmax
 //         states are joined in the epilogue.  One slot alone would leave the softmax of a tile
 //         and its two MMAs in series (~2300 cycles a tile against ~1450 of HBM time at 8 bits).
+//         So does a PAIR kernel over a coded cache with a sequence whose drafts fit one slot (MIXED): of up to 25
+//         drafts (b8 g7 t10007 INT8), 18 in every sequence took 77 us with one slot idle and take 59, one 67 and 56.
 //
 // Work.  The (sequence, KV head, 128-key tile) triples in that order are one line of W tiles, cut into
 // equal contiguous ranges, one per CTA (one per n_rb neighbouring CTAs): ragged lengths leave no CTA
@@ -104,6 +106,7 @@ struct TreePiece {
   int len, qn;        // the sequence's cache length and drafted tokens
   int which;          // 0: the first piece of this CTA's range, 1: a later one (names its partial)
   bool whole;         // every tile of the item
+  int idx, joins;     // softmax warps: earlier pieces, those whose tiles the slots took in turn
 };
 
 // The pieces of a CTA's range, in order; every role walks its own copy.
@@ -142,6 +145,7 @@ struct TreeWalk {
     out.len = len;
     out.qn = qn;
     out.which = idx > 0;
+    out.idx = idx;
     out.whole = n == tiles;
     ++idx;
     left -= n;
@@ -198,6 +202,8 @@ __device__ __forceinline__ void tree_find_range(const TreeParams& p, int g, int 
 template <int KIND, int D, bool PAIR>
 struct TreeCfg {
   static constexpr bool CODED = KIND != TREE_BF16;
+  // A sequence of fewer drafts than n_q may need one row slot only.  bf16 has no shared memory left for the join.
+  static constexpr bool MIXED = PAIR && CODED;
   static constexpr int BOX_BYTES = 128 * 128;  // 128 rows x 64 bf16
   static constexpr int NBOX = D / 64;
   static constexpr int TILE_BYTES = NBOX * BOX_BYTES;
@@ -212,7 +218,7 @@ struct TreeCfg {
   static constexpr int OFF_RAW = OFF_U + NU * TILE_BYTES;
   static constexpr int OFF_SC = OFF_RAW + NR * RAW_BYTES;      // [NS][3][128] floats
   static constexpr int OFF_ML = OFF_SC + NS * (1536 + 32);            // [2 slots][128] (max, sum) of the halves
-  static constexpr int OFF_WALK = OFF_ML + (PAIR ? 0 : 2048);  // [8] walks, [8] pieces of the softmax warps
+  static constexpr int OFF_WALK = OFF_ML + (PAIR && !MIXED ? 0 : 2048);  // [8] walks, [8] pieces of the softmax warps
   static constexpr int OFF_BAR = OFF_WALK + 8 * (int)(sizeof(TreeWalk) + sizeof(TreePiece));
   static constexpr int N_BARS = 3 + 2 * NU + 2 * NR + 2 * NS + 2 + 2 + 2 + 2 + 1 + 1;
   static constexpr int SMEM_BYTES = OFF_BAR + N_BARS * 8 + 72 + 1024;  // + walk start, flags, alignment slack
@@ -360,7 +366,7 @@ __global__ void __launch_bounds__((TreeCfg<KIND, D, PAIR>::THREADS), 1)
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   uint64_t* bars = reinterpret_cast<uint64_t*>(smem + C::OFF_BAR);
-  // Phases: q_*, o_*, ml_* complete once per piece (qi); u_full / u_empty once per use of a unit (u);
+  // Phases: q_*, o_* complete once per piece (qi); u_full / u_empty once per use of a unit (u);
   // raw_* once per raw unit, sc_* once per tile, s_full / p_full once per tile of their slot.
   uint64_t* q_full = bars;
   uint64_t* q_empty = bars + 1;
@@ -375,7 +381,7 @@ __global__ void __launch_bounds__((TreeCfg<KIND, D, PAIR>::THREADS), 1)
   uint64_t* p_full = s_full + 2;        // [2]
   uint64_t* o_full = p_full + 2;
   uint64_t* o_empty = o_full + 1;
-  uint64_t* ml_full = o_empty + 1;      // the halves' (max, sum) are in shared memory (8 warps)
+  uint64_t* ml_full = o_empty + 1;      // the halves' (max, sum) are in shared memory (8 warps; once per joined piece)
   uint64_t* ml_empty = ml_full + 1;     // ... and have been read
   uint64_t* drain = ml_empty + 1;
   uint64_t* q_meet = drain + 1;         // the converter warps' q_max are in shared memory
@@ -390,6 +396,10 @@ __global__ void __launch_bounds__((TreeCfg<KIND, D, PAIR>::THREADS), 1)
   const int warp = threadIdx.x >> 5;
   const int lane = threadIdx.x & 31;
   const int rb = (int)blockIdx.x % p.n_rb;
+  // Whether the two slots hold different rows of this piece (else they take its tiles in turn).
+  auto paired = [&](const TreePiece& it) -> bool {
+    return PAIR && (!C::MIXED || it.qn > (rb * 2 + 1) * p.tps);
+  };
   grid_launch_dependents();  // tree_join's CTAs find room as this kernel's leave
 
   if (threadIdx.x == 0) {
@@ -474,7 +484,7 @@ __global__ void __launch_bounds__((TreeCfg<KIND, D, PAIR>::THREADS), 1)
           for (int bx = 0; bx < C::NBOX; ++bx)
             tma_load_5d(smem + C::OFF_Q + s * C::TILE_BYTES + bx * C::BOX_BYTES, &tmQ, q_land, bx * 64, 0,
                         (rb * C::NQ + s) * p.tps, it.kvh, it.b);
-        if constexpr (PAIR) {
+        if (paired(it)) {
           for (int j = 0; j < it.n && ok; ++j) ok = load(&tmK, it, j) && load(&tmV, it, j);
         } else {
           ok = load(&tmK, it, 0) && (it.n < 2 || load(&tmK, it, 1));
@@ -503,8 +513,8 @@ __global__ void __launch_bounds__((TreeCfg<KIND, D, PAIR>::THREADS), 1)
       const uint32_t q_lo = sdesc_sw128_lo(smem_u32(smem + C::OFF_Q), 16);
       const uint32_t k_lo = sdesc_sw128_lo(smem_u32(smem + C::OFF_U), 16);
       const uint32_t v_lo = sdesc_sw128_lo(smem_u32(smem + C::OFF_U), C::BOX_BYTES);
-      auto issue_qk = [&](int s, int st) {
-        const uint32_t a0 = q_lo + (((PAIR ? s : 0) * C::TILE_BYTES) >> 4), b0 = k_lo + ((st * C::TILE_BYTES) >> 4);
+      auto issue_qk = [&](int s, int qs, int st) {
+        const uint32_t a0 = q_lo + ((qs * C::TILE_BYTES) >> 4), b0 = k_lo + ((st * C::TILE_BYTES) >> 4);
         const uint32_t d = tmem + s * 128;
 #pragma unroll
         for (int kk = 0; kk < D / 16; ++kk) {
@@ -535,14 +545,14 @@ __global__ void __launch_bounds__((TreeCfg<KIND, D, PAIR>::THREADS), 1)
         const int n = it.n;
         int st = 0;
         if (!(ok = mbar_wait_warp<true>(q_full, qi & 1, SITE_TR_MMA_Q))) break;
-        if constexpr (PAIR) {
+        if (paired(it)) {
           if (!(ok = wait_unit(st))) break;
           tc_fence_after();
           // S(0) of this piece overwrites S/P regions the previous piece's PVs read: those were
           // issued earlier by this warp and the tensor pipe executes in order.
-          issue_qk(0, st);
+          issue_qk(0, 0, st);
           mma_commit_elect(&s_full[0]);
-          issue_qk(1, st);
+          issue_qk(1, 1, st);
           mma_commit_elect(&s_full[1]);
           mma_commit_elect(&u_empty[st]);
           if (n == 1) mma_commit_elect(q_empty);
@@ -557,26 +567,27 @@ __global__ void __launch_bounds__((TreeCfg<KIND, D, PAIR>::THREADS), 1)
             if (more) {
               if (!(ok = wait_unit(sk))) break;
               tc_fence_after();
-              issue_qk(0, sk);
+              issue_qk(0, 0, sk);
               mma_commit_elect(&s_full[0]);
             }
-            if (!(ok = mbar_wait_warp<true>(&p_full[1], c0 & 1, SITE_TR_MMA_P))) break;
+            if (!(ok = mbar_wait_warp<true>(&p_full[1], c1 & 1, SITE_TR_MMA_P))) break;
             tc_fence_after();
             issue_pv(1, sv, j > 0);
             mma_commit_elect(&u_empty[sv]);
             if (more) {
-              issue_qk(1, sk);
+              issue_qk(1, 1, sk);
               mma_commit_elect(&s_full[1]);
               mma_commit_elect(&u_empty[sk]);
               if (j + 2 == n) mma_commit_elect(q_empty);
             }
             ++c0;
+            ++c1;
           }
         } else {
           for (int s = 0; s < 2 && s < n; ++s) {
             if (!(ok = wait_unit(st))) break;
             tc_fence_after();
-            issue_qk(s, st);
+            issue_qk(s, 0, st);
             mma_commit_elect(&s_full[s]);
             mma_commit_elect(&u_empty[st]);
           }
@@ -593,7 +604,7 @@ __global__ void __launch_bounds__((TreeCfg<KIND, D, PAIR>::THREADS), 1)
             if (j + 2 < n) {
               if (!(ok = wait_unit(st))) break;
               tc_fence_after();
-              issue_qk(s, st);
+              issue_qk(s, 0, st);
               mma_commit_elect(&s_full[s]);
               mma_commit_elect(&u_empty[st]);
               if (j + 3 == n) mma_commit_elect(q_empty);
@@ -828,11 +839,12 @@ __global__ void __launch_bounds__((TreeCfg<KIND, D, PAIR>::THREADS), 1)
       w.init(p, walk0);
       while (ok && w.next(p, it)) {
         const int n = it.n;
+        const bool duo = paired(it);
         ok = convert_q(it);
         for (int x = 0; x < 2 * n && ok; ++x) {  // the units of the piece, in the order of tree_v_unit
           bool is_v;
           int j;
-          if constexpr (PAIR) {
+          if (duo) {
             is_v = x & 1;
             j = x >> 1;
           } else {
@@ -853,9 +865,9 @@ __global__ void __launch_bounds__((TreeCfg<KIND, D, PAIR>::THREADS), 1)
     const uint32_t lane_off = (uint32_t)(wq * 32) << 16;
     const uint32_t tS = tmem + slot * 128 + lane_off;
     const uint32_t tO = tmem + 256 + slot * D + lane_off;
-    const int tok_i = (rb * C::NQ + (PAIR ? slot : 0)) * p.tps + r / p.G;  // this row's drafted token
+    const int tok_0 = (rb * C::NQ + (PAIR && !C::MIXED ? slot : 0)) * p.tps + r / p.G;
     const int head_g = r % p.G;
-    const bool row_used = r < p.tps * p.G && tok_i < p.n_q;
+    const bool row_used = r < p.tps * p.G && tok_0 < p.n_q;
     int cs = 0, g = 0, qi = 0, ub = 0;  // tiles of this slot, tiles of the CTA, pieces, units before this piece
     bool ok = true;
     // The walk and its piece are kept in shared memory, a copy per warp: between pieces they are dead weight,
@@ -868,6 +880,8 @@ __global__ void __launch_bounds__((TreeCfg<KIND, D, PAIR>::THREADS), 1)
       else w = sw;
       TreePiece x;
       const bool more = w.next(p, x);
+      if constexpr (C::MIXED) x.joins = first ? 0 : it.joins + !paired(it);
+      else x.joins = x.idx;
       __syncwarp();  // every lane has read the old walk and piece
       if (lane == 0 && more) {
         sw = w;
@@ -878,6 +892,8 @@ __global__ void __launch_bounds__((TreeCfg<KIND, D, PAIR>::THREADS), 1)
     };
     while (ok && next_piece(qi == 0)) {
       const int n = it.n, t0 = it.t0, base = it.len - it.qn;
+      const bool duo = paired(it);
+      const int tok_i = tok_0 + (C::MIXED && duo ? slot * p.tps : 0);  // this row's drafted token
       const bool row_ok = row_used && tok_i < it.qn;
       // This row's mask, read where it is needed (the last tiles of a sequence): no registers in the loop.
       auto row_mask = [&]() -> unsigned long long {
@@ -886,7 +902,7 @@ __global__ void __launch_bounds__((TreeCfg<KIND, D, PAIR>::THREADS), 1)
       };
       float m_used = -INFINITY, l = 0.f;
       const bool piece_used = __any_sync(0xffffffffu, row_ok);  // else this warp's rows of S, P and O are nobody's
-      for (int j = PAIR ? 0 : slot; j < n; j += PAIR ? 1 : 2) {
+      for (int j = duo ? 0 : slot; j < n; j += duo ? 1 : 2) {
         // tcgen05.ld/st are warp-collective: every lane takes the same branch around them.
         if (!(ok = mbar_wait_warp<true>(&s_full[slot], cs & 1, SITE_TR_SM_S))) break;
         tc_fence_after();
@@ -897,6 +913,7 @@ __global__ void __launch_bounds__((TreeCfg<KIND, D, PAIR>::THREADS), 1)
             const int ss = (g + j) % C::NS;
             if (!(ok = mbar_wait_warp<true>(&sc_full[ss], ((g + j) / C::NS) & 1, SITE_TR_SM_SC))) break;
             if (lane == 0) mbar_arrive(&sc_empty[ss]);
+            if (C::MIXED && !duo && lane == 0) mbar_arrive(&sc_empty[ss]);  // for the other slot's warp too
           }
           if (lane == 0) mbar_arrive(&p_full[slot]);
           ++cs;
@@ -1008,7 +1025,7 @@ __global__ void __launch_bounds__((TreeCfg<KIND, D, PAIR>::THREADS), 1)
             l *= alpha;
             m_used = m_new;
           }
-          if (j > (PAIR ? 0 : slot)) {  // the whole warp rescales its 32 rows of O (factor 1 where unchanged)
+          if (j > (duo ? 0 : slot)) {  // the whole warp rescales its 32 rows of O (factor 1 where unchanged)
 #pragma unroll 1
             for (int c = 0; c < D / 32; ++c) {
               uint32_t orow[32];
@@ -1114,7 +1131,10 @@ __global__ void __launch_bounds__((TreeCfg<KIND, D, PAIR>::THREADS), 1)
         __syncwarp();
         if (lane == 0) {
           mbar_arrive(&p_full[slot]);
-          if constexpr (CODED) mbar_arrive(&sc_empty[(g + j) % C::NS]);
+          if constexpr (CODED) {
+            mbar_arrive(&sc_empty[(g + j) % C::NS]);
+            if (C::MIXED && !duo) mbar_arrive(&sc_empty[(g + j) % C::NS]);
+          }
         }
         if constexpr (!CODED) {  // after P is handed over: the MMA does not wait for it
 #pragma unroll
@@ -1126,18 +1146,18 @@ __global__ void __launch_bounds__((TreeCfg<KIND, D, PAIR>::THREADS), 1)
         ++cs;
       }
       if (!ok) break;
-      // ---- epilogue.  Weights of this slot's and the other half's O (PAIR: of this slot's alone).
+      // ---- epilogue.  Weights of this slot's and the other half's O (paired: of this slot's alone).
       float f_own, f_other = 0.f, lse2;
-      if constexpr (PAIR) {
+      if (duo) {
         f_own = l == 0.f ? 0.f : 1.f / l;
         lse2 = l == 0.f ? -INFINITY : m_used + log2f(l);
       } else {
         float2* ml = reinterpret_cast<float2*>(smem + C::OFF_ML);
-        if (qi > 0 && !(ok = mbar_wait_warp<true>(ml_empty, (qi - 1) & 1, SITE_TR_EPI))) break;
+        if (it.joins > 0 && !(ok = mbar_wait_warp<true>(ml_empty, (it.joins - 1) & 1, SITE_TR_EPI))) break;
         ml[slot * 128 + r] = make_float2(m_used, l);
         __syncwarp();
         if (lane == 0) mbar_arrive(ml_full);
-        if (!(ok = mbar_wait_warp<true>(ml_full, qi & 1, SITE_TR_EPI))) break;
+        if (!(ok = mbar_wait_warp<true>(ml_full, it.joins & 1, SITE_TR_EPI))) break;
         const float2 other = ml[(slot ^ 1) * 128 + r];
         __syncwarp();
         if (lane == 0) mbar_arrive(ml_empty);
@@ -1154,20 +1174,20 @@ __global__ void __launch_bounds__((TreeCfg<KIND, D, PAIR>::THREADS), 1)
       const bool fix = *reinterpret_cast<volatile int*>(odd_piece + (qi & 7)) == qi + 1;
       const long long orow = ((long long)it.b * p.n_q + tok_i) * p.Hq + (long long)it.kvh * p.G + head_g;
       const long long part = (long long)blockIdx.x * 2 + it.which;
-      const int prow = (PAIR ? slot * 128 : 0) + r;
-      // PAIR: each slot stores its rows' D columns; halves: each slot stores half the columns of every row.
-      constexpr int NCH = PAIR ? D / 32 : D / 64;
-      const int ch0 = PAIR ? 0 : slot * NCH;
+      const int prow = (duo ? slot * 128 : 0) + r;
+      // Paired: each slot stores its rows' D columns; halves: each slot stores half the columns of every row.
+      const int n_ch = duo ? D / 32 : D / 64;
+      const int ch0 = duo ? 0 : slot * n_ch;
       if (CODED && !piece_used && lane == 0) mbar_arrive(o_empty);
 #pragma unroll 1
-      for (int c = ch0; c < ch0 + NCH && (piece_used || !CODED); ++c) {
+      for (int c = ch0; c < ch0 + n_ch && (piece_used || !CODED); ++c) {
         uint32_t ov[32];
         tmem_ld32(tO + c * 32, ov);
         tmem_wait_ld_regs(ov);
 #pragma unroll
         for (int i = 0; i < 32; ++i)  // an O that no PV wrote is not read into the sum
           ov[i] = f_own == 0.f ? 0u : __float_as_uint(__uint_as_float(ov[i]) * f_own);
-        if constexpr (!PAIR) {
+        if (!duo) {
           uint32_t o2[32];
           tmem_ld32(tmem + 256 + (slot ^ 1) * D + lane_off + c * 32, o2);
           tmem_wait_ld_regs(o2);
@@ -1176,7 +1196,7 @@ __global__ void __launch_bounds__((TreeCfg<KIND, D, PAIR>::THREADS), 1)
             if (f_other != 0.f)
               ov[i] = __float_as_uint(fmaf(__uint_as_float(o2[i]), f_other, __uint_as_float(ov[i])));
         }
-        if (c == ch0 + NCH - 1) {  // O has been read: the next piece's first PV may overwrite it
+        if (c == ch0 + n_ch - 1) {  // O has been read: the next piece's first PV may overwrite it
           tc_fence_before();
           __syncwarp();
           if (lane == 0) mbar_arrive(o_empty);
@@ -1221,7 +1241,7 @@ __global__ void __launch_bounds__((TreeCfg<KIND, D, PAIR>::THREADS), 1)
           }
         }
       }
-      if (row_ok && (PAIR || slot == 0)) {
+      if (row_ok && (duo || slot == 0)) {
         if (!it.whole) p.part_lse[part * C::ROWS + prow] = lse2;
         else if (p.lse) p.lse[orow] = lse2 * 0.69314718055994531f;
       }
