@@ -30,8 +30,10 @@
 // every code (one instruction per two E4M3 codes, five per four INT8 codes; bf16 took five and eight);
 // the queries follow as f16 times a power of two.  The K scale multiplies the fp32 score and the V
 // scale the fp32 weight before its one rounding to f16, so no scale is rounded.  A row's weights are
-// taken relative to its largest weight times V scale, max_t (y_t + log2 |v_scale_t|), not to its largest weight:
-// the products are at most 2^8 and the large ones keep f16's full precision whatever the scales.
+// taken relative to its largest weight times V scale, max_t (y_t + log2 |v_scale_t|), not to its largest weight,
+// and from a reference REF_DROP powers of two below it, in f16's upper range: the row's largest product is 2^3 to
+// 2^15, so products down to 2^-17 of it keep f16's full precision whatever the scales and those below are off by
+// at most 2^-28 of it.  (With the largest at 2^-8 to 2^8 a sink token over 128K flat ones cost half of the others' part.)
 //
 // Masked places.  Slots past kv_len and drafts no token sees are never used.  A draft that some tokens
 // see may hold anything too: its non-finite V elements enter the MMA as zeros (0 * NaN would reach
@@ -236,7 +238,14 @@ struct TreeCfg {
   // largest and smallest of K's and of the logarithms.
   static constexpr int SC_BYTES = 3 * 512 + 32;
   static constexpr uint32_t TMEM_COLS = 512;
-  static constexpr float RESCALE_THRESHOLD = 8.0f;
+  // A row's reference may lag its maximum by RESCALE_THRESHOLD and lies REF_DROP below (an upper bound of) it:
+  // products reach 2^(4 + 11), of f16's 65504.  A bound may exceed the maximum by REF_SLACK, so the largest
+  // product is at least 2^(11 - 8).  A sum of weights stays below 2^(15 + LOG_MIN's 80) a token.  Measured (b8 n16
+  // t32768 FP8, INT8, INT4 on N(0, 1) values): 203, 218, 214 us with thresholds of 8, drops of 7 and slacks of 8 (floor 2^-24);
+  // 205, 219, 215 as it is (2^-28); 211, 225, 223 with slacks of 7, which send more tiles column by column.
+  static constexpr float RESCALE_THRESHOLD = CODED ? 4.0f : 8.0f;
+  static constexpr float REF_DROP = 11.0f, REF_SLACK = 8.0f;
+  static constexpr float LOG_MIN = -80.0f, LOG_MAX = 100.0f;  // of log2 |V scale|
   static constexpr int ROWS = PAIR ? 256 : 128;  // rows of a partial
 };
 
@@ -669,7 +678,7 @@ __global__ void __launch_bounds__((TreeCfg<KIND, D, PAIR>::THREADS), 1)
             }
             dst[t] = ks[x] * kf;
             dst[128 + t] = vs[x];
-            dst[256 + t] = fminf(fmaxf(__log2f(fabsf(vs[x])), -100.f), 100.f);
+            dst[256 + t] = fminf(fmaxf(__log2f(fabsf(vs[x])), C::LOG_MIN), C::LOG_MAX);
           }
           uint32_t k1 = 0, k0 = 0x7f800000u, v1 = 0, v0 = 0x7f800000u;
           bool odd = false;  // K scales that are negative or not finite
@@ -690,8 +699,8 @@ __global__ void __launch_bounds__((TreeCfg<KIND, D, PAIR>::THREADS), 1)
           if (lane == 0) {
             dst[384 + (warp - 2) * 4] = __uint_as_float(k1);
             dst[385 + (warp - 2) * 4] = odd ? -INFINITY : __uint_as_float(k0);
-            dst[386 + (warp - 2) * 4] = fminf(fmaxf(__log2f(__uint_as_float(v1)), -100.f), 100.f);
-            dst[387 + (warp - 2) * 4] = fminf(fmaxf(__log2f(__uint_as_float(v0)), -100.f), 100.f);
+            dst[386 + (warp - 2) * 4] = fminf(fmaxf(__log2f(__uint_as_float(v1)), C::LOG_MIN), C::LOG_MAX);
+            dst[387 + (warp - 2) * 4] = fminf(fmaxf(__log2f(__uint_as_float(v0)), C::LOG_MIN), C::LOG_MAX);
           }
           if (j + 1 < it.n) fetch(it, j + 1);
           __syncwarp();
@@ -945,8 +954,8 @@ __global__ void __launch_bounds__((TreeCfg<KIND, D, PAIR>::THREADS), 1)
           if (!edge) {
             // The largest bare product times the largest (a negative one: the smallest) K scale, plus the largest
             // log2 |V scale|, bounds the largest sum from above, and from no further than that product times the
-            // K scales' range plus the logarithms' range.  Any reference within a few powers of two of the
-            // maximum serves; columns are looked at one by one only where it is not.
+            // K scales' range plus the logarithms' range.  A reference within REF_SLACK of the maximum serves;
+            // columns are looked at one by one only where it may be farther.
 #pragma unroll 1
             for (int h = 0; h < 2; ++h) {
               tmem_ld32(tS + h * 64, h0);
@@ -968,7 +977,7 @@ __global__ void __launch_bounds__((TreeCfg<KIND, D, PAIR>::THREADS), 1)
             mx0 = fmaf(top, top >= 0.f ? k_max : k_min, g_max);
             mx1 = mx2 = mx3 = -INFINITY;
             // Lanes without a row hold anything, and must not sway which way (and so which rounding) the others take.
-            by_column = !__all_sync(0xffffffffu, !row_ok || fmaf(fabsf(top), k_max - k_min, g_max - g_min) <= 8.f);
+            by_column = !__all_sync(0xffffffffu, !row_ok || fmaf(fabsf(top), k_max - k_min, g_max - g_min) <= C::REF_SLACK);
           }
           if (by_column) {
             mx0 = -INFINITY;
@@ -1016,7 +1025,8 @@ __global__ void __launch_bounds__((TreeCfg<KIND, D, PAIR>::THREADS), 1)
           }
         }
         // Scores in units of log2: the staged K scales of a coded cache hold the factor already.
-        const float m_tile = fmaxf(fmaxf(mx0, mx1), fmaxf(mx2, mx3)) * (CODED ? 1.f : p.scale_log2);
+        const float mx = fmaxf(fmaxf(mx0, mx1), fmaxf(mx2, mx3));
+        const float m_tile = CODED ? mx - C::REF_DROP : mx * p.scale_log2;
         const float m_new = fmaxf(m_used, m_tile);
         const bool need = m_new > m_used + C::RESCALE_THRESHOLD;
         if (__any_sync(0xffffffffu, need)) {
@@ -1081,8 +1091,8 @@ __global__ void __launch_bounds__((TreeCfg<KIND, D, PAIR>::THREADS), 1)
                     make_float2(ex2_approx(__uint_as_float(x[2 * i + 2])), ex2_approx(__uint_as_float(x[2 * i + 3])));
                 add_sum(i, e0);
                 add_sum(i + 1, e1);
-                // The weight times its V scale is rounded once, to f16 (at most 2^-11 of it, or 2^-25 of the row's
-                // largest such product).
+                // The weight times its V scale is rounded once, to f16 (at most 2^-11 of it, or 2^-28 of the row's
+                // largest such product: see REF_DROP).
                 e0 = mul2(e0, make_float2(v4[i / 2].x, v4[i / 2].y));
                 e1 = mul2(e1, make_float2(v4[i / 2].z, v4[i / 2].w));
                 pk[i] = pack_f16x2(e0.x, e0.y);
