@@ -42,7 +42,12 @@ __device__ __forceinline__ void record_arg_error(uint32_t code, int site) {
 
 // ---------------------------------------------------------------- shared memory by address
 
-// 16 bytes from a shared-memory address.
+// 4 or 16 bytes from a shared-memory address.
+__device__ __forceinline__ float lds_f1(uint32_t addr) {
+  float v;
+  asm volatile("ld.shared.f32 %0, [%1];" : "=f"(v) : "r"(addr));
+  return v;
+}
 __device__ __forceinline__ float4 lds_f4(uint32_t addr) {
   float4 v;
   asm volatile("ld.shared.v4.f32 {%0, %1, %2, %3}, [%4];" : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w) : "r"(addr));

@@ -28,7 +28,8 @@
 // O += P V; unit ring of MMA-ready K and V tiles in consumption order.  Coded caches (E4M3, INT8, INT4)
 // land raw in a ring of their own and a fourth warpgroup widens them to f16, which is exact for
 // every code (one instruction per two E4M3 codes, five per four INT8 codes; bf16 took five and eight);
-// the queries follow as f16 times a power of two.  The K scale multiplies the fp32 score and the V
+// the queries follow as f16 times a power of two, one for all of a piece's rows but those far below its largest,
+// which get their own (a padded draft's query may be anything, and is nobody else's business).  The K scale multiplies the fp32 score and the V
 // scale the fp32 weight before its one rounding to f16, so no scale is rounded.  A row's weights are
 // taken relative to its largest weight times V scale, max_t (y_t + log2 |v_scale_t|), not to its largest weight,
 // and from a reference REF_DROP powers of two below it, in f16's upper range: the row's largest product is 2^3 to
@@ -223,7 +224,8 @@ struct TreeCfg {
   static constexpr int OFF_WALK = OFF_ML + (PAIR && !MIXED ? 0 : 2048);  // [8] walks, [8] pieces of the softmax warps
   static constexpr int OFF_BAR = OFF_WALK + 8 * (int)(sizeof(TreeWalk) + sizeof(TreePiece));
   static constexpr int N_BARS = 3 + 2 * NU + 2 * NR + 2 * NS + 2 + 2 + 2 + 2 + 1 + 1;
-  static constexpr int SMEM_BYTES = OFF_BAR + N_BARS * 8 + 72 + 1024;  // + walk start, flags, alignment slack
+  static constexpr int OFF_ROWF = OFF_BAR + N_BARS * 8 + 72;  // + walk start, flags; [2 pieces][NQ][128] row factors
+  static constexpr int SMEM_BYTES = OFF_ROWF + (CODED ? 2 * NQ * 512 : 0) + 1024;  // + alignment slack
   static constexpr int THREADS = CODED ? 512 : 384;
   // Register split: the softmax holds a row's 128 scores (bf16) or half of them (coded caches, of whose 512
   // threads a launch has 128 registers each), and the other warpgroups give up what that takes.  The sum
@@ -401,6 +403,9 @@ __global__ void __launch_bounds__((TreeCfg<KIND, D, PAIR>::THREADS), 1)
   int* odd_piece = walk0 + 3;
   uint32_t* q_max = reinterpret_cast<uint32_t*>(odd_piece + 8);  // [4] largest |q| (bf16 bits) per converter warp
   float* q_down = reinterpret_cast<float*>(q_max + 4);  // what undoes the queries' power of two
+  // What takes a row's scores to that power, by piece parity: its readers are done with piece i before the MMA has done
+  // the scores of piece i + 1 (every P of i comes first), which the queries of piece i + 2 wait for.
+  float* row_factor = reinterpret_cast<float*>(smem + C::OFF_ROWF);
 
   const int warp = threadIdx.x >> 5;
   const int lane = threadIdx.x & 31;
@@ -780,27 +785,41 @@ __global__ void __launch_bounds__((TreeCfg<KIND, D, PAIR>::THREADS), 1)
         return true;
       };
       // The piece's queries, bf16 -> f16 in place, times a power of two that takes the largest |q| to
-      // [2^14, 2^15).  What falls below f16's normal range is then off by at most 2^-39 of the largest,
-      // far less than fp32 accumulation loses on it.
+      // [2^14, 2^15).  What falls below f16's normal range is then off by at most 2^-39 of the largest.  A row whose
+      // own largest is more than 2^14 below that (2^-25 of its own, as little as fp32 accumulation loses on it) is taken
+      // there by a power of two of its own, whose ratio to the common one the softmax multiplies its scores by.
+      // Thread t holds 16-byte chunk t & 7 of rows t >> 3, + 16, ...: a row belongs to eight lanes of a warp.
+      auto q_shift = [](uint32_t top) -> int { return min(14 + 127 - max((int)(top >> 7), 1), 127); };
       auto convert_q = [&](const TreePiece& it) -> bool {
         if (!mbar_wait_warp<true>(q_raw, qi & 1, SITE_TR_CONV)) return false;
         // Only rows of drafts there are: nobody looks at the others, nor at what they turn into.
         const uint32_t qs = smem_u32(smem + C::OFF_Q) + t * 16;
+        float* const rowf = row_factor + (qi & 1) * C::NQ * 128;  // first the rows' largest |q|, as bf16 bits
         uint32_t top = 0;
 #pragma unroll 1
-        for (int x = 0; x < C::NQ * C::NBOX; ++x) {
-          const int chunks = min(max(it.qn - (rb * C::NQ + x / C::NBOX) * p.tps, 0), p.tps) * p.G * 8;
-          const uint32_t at = qs + x * C::BOX_BYTES;
-#pragma unroll 4
-          for (int i = t; i < chunks; i += 128) {
-            const uint4 v = lds_u4(at + (i - t) * 16);
-            const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+        for (int s = 0; s < C::NQ; ++s) {
+          const int rows = min(max(it.qn - (rb * C::NQ + s) * p.tps, 0), p.tps) * p.G;
+#pragma unroll 1
+          for (int r0 = 0; r0 + cw * 4 < rows; r0 += 16) {
+            const int r = r0 + (t >> 3);
+            uint32_t m = 0;
+            if (r < rows) {
 #pragma unroll
-            for (int k = 0; k < 4; ++k) {
-              const uint32_t lo = w[k] & 0x7fffu, hi = (w[k] >> 16) & 0x7fffu;
-              if (lo < 0x7f80u) top = max(top, lo);
-              if (hi < 0x7f80u) top = max(top, hi);
+              for (int x = 0; x < C::NBOX; ++x) {
+                const uint4 v = lds_u4(qs + s * C::TILE_BYTES + x * C::BOX_BYTES + r0 * 128);
+                const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {
+                  const uint32_t lo = w[k] & 0x7fffu, hi = (w[k] >> 16) & 0x7fffu;
+                  if (lo < 0x7f80u) m = max(m, lo);
+                  if (hi < 0x7f80u) m = max(m, hi);
+                }
+              }
             }
+#pragma unroll
+            for (int o = 1; o < 8; o <<= 1) m = max(m, __shfl_xor_sync(0xffffffffu, m, o));
+            if ((lane & 7) == 0 && r < rows) rowf[s * 128 + r] = __uint_as_float(m);
+            top = max(top, m);
           }
         }
         top = __reduce_max_sync(0xffffffffu, top);
@@ -811,31 +830,42 @@ __global__ void __launch_bounds__((TreeCfg<KIND, D, PAIR>::THREADS), 1)
         // Not a named barrier, whose wait has no limit should another warp have given up.
         if (!mbar_wait_warp<true>(q_meet, qi & 1, SITE_TR_CONV)) return false;
         top = max(max(q_max[0], q_max[1]), max(q_max[2], q_max[3]));
-        const int shift = min(14 + 127 - max((int)(top >> 7), 1), 127);
-        const float up = __uint_as_float((uint32_t)(127 + shift) << 23);
+        const int shift = q_shift(top);
         if (t == 0) *q_down = exp2f((float)-shift);
 #pragma unroll 1
-        for (int x = 0; x < C::NQ * C::NBOX; ++x) {
-          const int chunks = min(max(it.qn - (rb * C::NQ + x / C::NBOX) * p.tps, 0), p.tps) * p.G * 8;
-          const uint32_t at = qs + x * C::BOX_BYTES;
-#pragma unroll 2
-          for (int i = t; i < chunks; i += 128) {
-            const uint4 v = lds_u4(at + (i - t) * 16);
-            const uint32_t w[4] = {v.x, v.y, v.z, v.w};
-            float f[8];
+        for (int s = 0; s < C::NQ; ++s) {
+          const int rows = min(max(it.qn - (rb * C::NQ + s) * p.tps, 0), p.tps) * p.G;
+#pragma unroll 1
+          for (int r0 = 0; r0 + cw * 4 < rows; r0 += 16) {
+            const int r = r0 + (t >> 3);
+            int row_shift = shift;
+            if (r < rows) {
+              const uint32_t m = __float_as_uint(rowf[s * 128 + r]);
+              if (m > 0 && (m >> 7) + 14 < (top >> 7)) row_shift = q_shift(m);
+              const float up = __uint_as_float((uint32_t)(127 + row_shift) << 23);
 #pragma unroll
-            for (int k = 0; k < 4; ++k) {
-              f[2 * k] = __uint_as_float(w[k] << 16) * up;
-              f[2 * k + 1] = __uint_as_float(w[k] & 0xffff0000u) * up;
+              for (int x = 0; x < C::NBOX; ++x) {
+                const uint32_t at = qs + s * C::TILE_BYTES + x * C::BOX_BYTES + r0 * 128;
+                const uint4 v = lds_u4(at);
+                const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+                float f[8];
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {
+                  f[2 * k] = __uint_as_float(w[k] << 16) * up;
+                  f[2 * k + 1] = __uint_as_float(w[k] & 0xffff0000u) * up;
+                }
+                uint4 h;
+                if constexpr (KIND == TREE_INT4)
+                  h = make_uint4(pack_f16x2(f[0], f[4]), pack_f16x2(f[1], f[5]), pack_f16x2(f[2], f[6]),
+                                 pack_f16x2(f[3], f[7]));
+                else
+                  h = make_uint4(pack_f16x2(f[0], f[1]), pack_f16x2(f[2], f[3]), pack_f16x2(f[4], f[5]),
+                                 pack_f16x2(f[6], f[7]));
+                sts_u4(at, h);
+              }
             }
-            uint4 h;
-            if constexpr (KIND == TREE_INT4)
-              h = make_uint4(pack_f16x2(f[0], f[4]), pack_f16x2(f[1], f[5]), pack_f16x2(f[2], f[6]),
-                             pack_f16x2(f[3], f[7]));
-            else
-              h = make_uint4(pack_f16x2(f[0], f[1]), pack_f16x2(f[2], f[3]), pack_f16x2(f[4], f[5]),
-                             pack_f16x2(f[6], f[7]));
-            sts_u4(at + (i - t) * 16, h);
+            __syncwarp();  // the row's largest has been read
+            if ((lane & 7) == 0 && r < rows) rowf[s * 128 + r] = row_shift == shift ? 1.f : exp2f((float)(shift - row_shift));
           }
         }
         fence_proxy_async_smem();
@@ -943,6 +973,8 @@ __global__ void __launch_bounds__((TreeCfg<KIND, D, PAIR>::THREADS), 1)
             if (!((see >> i) & 1u)) x[i] = __float_as_uint(-INFINITY);
         };
         uint32_t sc = 0;  // shared address of the tile's scales
+        bool rescaled = false;  // coded caches: a row of this warp has a power of two of its own
+        const uint32_t row_at = smem_u32(row_factor) + (((qi & 1) * C::NQ + (PAIR && duo ? slot : 0)) * 128 + r) * 4;
         float mx0 = -INFINITY, mx1 = -INFINITY, mx2 = -INFINITY, mx3 = -INFINITY;
         if constexpr (CODED) {
           const int ss = (g + j) % C::NS;
@@ -950,6 +982,7 @@ __global__ void __launch_bounds__((TreeCfg<KIND, D, PAIR>::THREADS), 1)
           uint32_t(&h0)[32] = *reinterpret_cast<uint32_t(*)[32]>(&sr[0]);
           uint32_t(&h1)[32] = *reinterpret_cast<uint32_t(*)[32]>(&sr[32]);
           sc = smem_u32(smem + C::OFF_SC) + ss * C::SC_BYTES;
+          const float rf = row_ok ? lds_f1(row_at) : 1.f;
           bool by_column = edge;
           if (!edge) {
             // The largest bare product times the largest (a negative one: the smallest) K scale, plus the largest
@@ -973,7 +1006,7 @@ __global__ void __launch_bounds__((TreeCfg<KIND, D, PAIR>::THREADS), 1)
             const float4 ha = lds_f4(sc + 1536), hb = lds_f4(sc + 1552);
             const float k_max = fmaxf(ha.x, hb.x), k_min = fminf(ha.y, hb.y);
             const float g_max = fmaxf(ha.z, hb.z), g_min = fminf(ha.w, hb.w);
-            const float top = fmaxf(fmaxf(mx0, mx1), fmaxf(mx2, mx3));
+            const float top = fmaxf(fmaxf(mx0, mx1), fmaxf(mx2, mx3)) * rf;
             mx0 = fmaf(top, top >= 0.f ? k_max : k_min, g_max);
             mx1 = mx2 = mx3 = -INFINITY;
             // Lanes without a row hold anything, and must not sway which way (and so which rounding) the others take.
@@ -989,9 +1022,10 @@ __global__ void __launch_bounds__((TreeCfg<KIND, D, PAIR>::THREADS), 1)
 #pragma unroll
               for (int i = 0; i < CH; i += 4) {
                 const float4 k4 = lds_f4(sc + (c * CH + i) * 4), g4 = lds_f4(sc + 1024 + (c * CH + i) * 4);
-                const float2 a = fma2(make_float2(__uint_as_float(x[i]), __uint_as_float(x[i + 1])),
+                const float2 f2 = make_float2(rf, rf);
+                const float2 a = fma2(mul2(make_float2(__uint_as_float(x[i]), __uint_as_float(x[i + 1])), f2),
                                       make_float2(k4.x, k4.y), make_float2(g4.x, g4.y));
-                const float2 b2 = fma2(make_float2(__uint_as_float(x[i + 2]), __uint_as_float(x[i + 3])),
+                const float2 b2 = fma2(mul2(make_float2(__uint_as_float(x[i + 2]), __uint_as_float(x[i + 3])), f2),
                                        make_float2(k4.z, k4.w), make_float2(g4.z, g4.w));
                 x[i] = __float_as_uint(a.x);
                 x[i + 1] = __float_as_uint(a.y);
@@ -1007,6 +1041,7 @@ __global__ void __launch_bounds__((TreeCfg<KIND, D, PAIR>::THREADS), 1)
             }
           }
           tmem_ld16(tS, chunk(0));  // for the weights
+          rescaled = __any_sync(0xffffffffu, rf != 1.f);  // not ahead of the loads of the scores: rf takes its time
         } else {
 #pragma unroll
           for (int c = 0; c < 4; ++c) tmem_ld32(tS + c * 32, chunk(c));
@@ -1057,8 +1092,14 @@ __global__ void __launch_bounds__((TreeCfg<KIND, D, PAIR>::THREADS), 1)
           a = add2(a, e);
         };
         if constexpr (CODED) {
-          // A masked tile has a copy of its own: selects in the common one cost 1500 cycles a tile.
+          // A masked tile has a copy of its own: selects in the common one cost 1500 cycles a tile.  Rows with a power of two
+          // of their own take it too.
           auto weights = [&](auto masked) {
+            const float rf = masked.value ? lds_f1(row_at) : 1.f;
+            auto scaled = [&](uint32_t a, uint32_t b) -> float2 {
+              const float2 y = make_float2(__uint_as_float(a), __uint_as_float(b));
+              return masked.value ? mul2(y, make_float2(rf, rf)) : y;
+            };
 #pragma unroll 2
             for (int c = 0; c < 8; ++c) {
               uint32_t(&x)[CH] = chunk(c);
@@ -1072,10 +1113,8 @@ __global__ void __launch_bounds__((TreeCfg<KIND, D, PAIR>::THREADS), 1)
               for (int i = 0; i < 4; ++i) v4[i] = lds_f4(sc + 512 + c * 64 + i * 16);
 #pragma unroll
               for (int i = 0; i < CH; i += 4) {
-                const float2 a = fma2(make_float2(__uint_as_float(x[i]), __uint_as_float(x[i + 1])),
-                                      make_float2(k4[i / 4].x, k4[i / 4].y), nm2);
-                const float2 b2 = fma2(make_float2(__uint_as_float(x[i + 2]), __uint_as_float(x[i + 3])),
-                                       make_float2(k4[i / 4].z, k4[i / 4].w), nm2);
+                const float2 a = fma2(scaled(x[i], x[i + 1]), make_float2(k4[i / 4].x, k4[i / 4].y), nm2);
+                const float2 b2 = fma2(scaled(x[i + 2], x[i + 3]), make_float2(k4[i / 4].z, k4[i / 4].w), nm2);
                 x[i] = __float_as_uint(a.x);
                 x[i + 1] = __float_as_uint(a.y);
                 x[i + 2] = __float_as_uint(b2.x);
@@ -1101,7 +1140,7 @@ __global__ void __launch_bounds__((TreeCfg<KIND, D, PAIR>::THREADS), 1)
               tmem_st8(tS + c * 8, pk);
             }
           };
-          if (edge) weights(std::true_type{});
+          if (edge || rescaled) weights(std::true_type{});
           else weights(std::false_type{});
         } else {
 #pragma unroll

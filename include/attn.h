@@ -240,6 +240,11 @@ ATTN_API attn_status_t attn_decode_paged(const void* q, const void* k_pool, cons
  *   q_lens     device int32 [B], each in [0, n_q], or NULL for n_q everywhere
  *   tree_mask  device int64 [B, n_q], 8-byte aligned; bits at or past q_lens[b] are ignored
  *   D          128, or 64 with a bf16 cache;  Hq / Hkv <= 128
+ *   values     a row is independent of the others' queries, whatever those hold.  Its scores scale * q.k should stay
+ *              below 2^25 in size (fp32 differences tell no more apart: the row alone may come out as NaN).  Coded
+ *              caches: each weight times its V scale is rounded once to f16, by at most 2^-11 of it or 2^-28 of the row's
+ *              largest such product, the greater (attn_decode_multi over FP8 keeps 16 bits); V scales up to 2^100
+ *              in size, and below 2^-80 as if they were 2^-80 when that largest product is chosen
  *   ws         at least attn_decode_tree_workspace_bytes(dims, Tmax, n_q) bytes on the device that will
  *              run the call (Tmax = max_pages * page_size when paged), 16-byte aligned, not shared by
  *              calls that may overlap; may be NULL when that size is 0

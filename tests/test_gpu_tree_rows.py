@@ -62,9 +62,9 @@ def rows_in_float64(q, kc, ks, vc, vs, mask, n_q):
             if not (int(mask[i]) >> (t - base)) & 1:
                 s[i, :, t] = -np.inf
     top = s.max(-1, keepdims=True)
-    e = np.exp(s - top)
-    w = e / e.sum(-1, keepdims=True)
-    return w @ v, (top + np.log(e.sum(-1, keepdims=True)))[..., 0], w @ np.abs(v)
+    e = np.exp(s - np.maximum(top, -1e300))
+    w = e / np.maximum(e.sum(-1, keepdims=True), 1e-300)
+    return w @ v, (top + np.log(np.maximum(e.sum(-1, keepdims=True), 1e-300)))[..., 0], w @ np.abs(v)
 
 
 def run_shared(kind, q, kc, ks, vc, vs, mask, dev):
@@ -122,4 +122,45 @@ def test_v_scales_of_next_to_nothing_over_a_long_cache(cuda_device, kind, n_q, t
     if tail == 0:
         assert (o == 0).all()
     check_rows(o, lse, [x + (1e-300 if i == 2 else 0) for i, x in enumerate(rows_in_float64(*c, mask, n_q))])
+    device_clean()
+
+
+@pytest.mark.parametrize("kind", CODED)
+@pytest.mark.parametrize("n_q,G", [(7, 4), (40, 4), (9, 1)])
+@pytest.mark.parametrize("big", [2.0**16, 2.0**40, 2.0**116])
+def test_a_row_of_huge_queries_leaves_the_others_alone(cuda_device, kind, n_q, G, big):
+    """Queries come as f16 relative to a power of two; a padded draft's may be anything (here of up to 2^116, whether
+    it sees nothing or the prefix), and one head's far from another's.  A row's own elements span 2^29 of
+    its largest exactly, so the ordinary rows keep the ordinary tolerance.  (The huge rows' own scores are
+    beyond what fp32 differences can tell apart, 2^25, and their outputs are not looked at.)"""
+    D, Hkv, dev = 128, 2, cuda_device
+    g = torch.Generator().manual_seed(n_q)
+    lens = [n_q, 700, 300]
+    T = max(lens)
+    kc, vc = (torch.randint(-7, 8, (3, T, Hkv, D), generator=g) for _ in range(2))
+    ks, vs = (0.1 * (1 + torch.rand(3, T, Hkv, generator=g)) for _ in range(2))
+    q = torch.randn(3, n_q, Hkv * G, D, generator=g).to(torch.bfloat16)
+    mask = np.array([[(1 << (i + 1)) - 1 for i in range(n_q)]] * 3, dtype=np.int64)
+    usual = torch.ones(3, n_q, Hkv * G, dtype=torch.bool)
+    for b in (0, 1):
+        for i in (2, n_q - 1):  # padding: sees no draft (in sequence 0, which is drafts alone, nothing)
+            mask[b, i] = 0
+            q[b, i] *= big
+            usual[b, i] = False
+    q[2, :, 0] *= big  # a head
+    usual[2, :, 0] = False
+    o, lse = A.attn_decode_tree(q.to(dev), encode(kc, kind).to(dev), encode(vc, kind).to(dev),
+                                torch.tensor(lens, dtype=torch.int32, device=dev), torch.from_numpy(mask).to(dev),
+                                k_scale=ks.to(dev), v_scale=vs.to(dev))
+    for b, n in enumerate(lens):
+        for h in range(Hkv):
+            heads = slice(h * G, (h + 1) * G)
+            ro, rl, size = rows_in_float64(q[b, :, heads], kc[b, :n, h], ks[b, :n, h], vc[b, :n, h], vs[b, :n, h],
+                                           mask[b], n_q)
+            u = usual[b, :, heads].numpy()
+            err = np.abs(to_np(o[b, :, heads]) - ro) / (2.0**-8 * np.abs(ro) + 2.0**-10 * size + 1e-300)
+            worst = err[u].max(initial=0.0)
+            assert worst <= 1, f"o: {worst:.3f} of its tolerance"
+            assert (np.abs(to_np(lse[b, :, heads])[u] - rl[u]) <= 2.0**-11 + 2.0**-20 * np.abs(rl[u])).all()
+    assert (o[0, 2] == 0).all() and torch.isneginf(lse[0, 2]).all()
     device_clean()
