@@ -550,6 +550,14 @@ def _cache(k, v, k_scale, v_scale):
     return layers, pages, page_size, Hkv, row * (1 if coded else 2)
 
 
+def _overlap(a, b) -> bool:
+    """Whether two contiguous tensors share memory (None shares none)."""
+    if a is None or b is None or a.numel() == 0 or b.numel() == 0:
+        return False
+    x, y = a.data_ptr(), b.data_ptr()
+    return x < y + b.numel() * b.element_size() and y < x + a.numel() * a.element_size()
+
+
 def _table(page_table):
     if page_table.dim() != 2:
         raise ValueError(f"page_table: expected int32 [B, max_pages], got shape {tuple(page_table.shape)}")
@@ -578,8 +586,11 @@ def attn_tree_accept(k, v, kv_lens, path, n_accepted, *, n_q: int | None = None,
         raise ValueError(f"k/v: expected {B} sequences (the length of kv_lens), got {pages}")
     if page_table is not None and _table(page_table)[0] != B:
         raise ValueError(f"page_table: expected {B} rows, got {page_table.shape[0]}")
-    if kv_lens_out is not None and kv_lens_out.data_ptr() == kv_lens.data_ptr():
-        raise ValueError("kv_lens_out: expected memory of its own, got kv_lens")
+    if kv_lens_out is not None:
+        for name, t in (("kv_lens", kv_lens), ("path", path), ("n_accepted", n_accepted), ("q_lens", q_lens),
+                        ("page_table", page_table)):
+            if _overlap(kv_lens_out, t):
+                raise ValueError(f"kv_lens_out: expected memory of its own, got some of {name}'s")
     with _On(device, stream) as st:
         if kv_lens_out is None:
             kv_lens_out = torch.empty_like(kv_lens)

@@ -39,6 +39,13 @@ static attn_status_t cuda_fail(cudaError_t e) {
 static bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 static bool aligned4(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
 
+// Whether two arrays of 4-byte elements share any byte (null or empty ones share none).
+static bool overlap4(const void* a, long long n_a, const void* b, long long n_b) {
+  if (!a || !b || n_a <= 0 || n_b <= 0) return false;
+  const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
+  return x < y + (uintptr_t)n_b * 4 && y < x + (uintptr_t)n_a * 4;
+}
+
 // ---------------------------------------------------------------- tensor maps
 
 typedef CUresult (*EncodeTiledFn)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*,
@@ -930,7 +937,7 @@ attn_status_t attn_tree_accept(void* k, void* v, float* k_scale, float* v_scale,
   if (B < 0 || n_q < 0 || n_layers < 0 || (page_table && (max_pages < 1 || page_size < 128 || page_size % 128 != 0)))
     return ATTN_ERR_INVALID_ARG;
   if (B == 0) return ATTN_OK;
-  if (!kv_lens || !path || !n_accepted || !kv_lens_out || kv_lens_out == kv_lens) return ATTN_ERR_INVALID_ARG;
+  if (!kv_lens || !path || !n_accepted || !kv_lens_out) return ATTN_ERR_INVALID_ARG;
   if (!aligned4(kv_lens) || !aligned4(path) || !aligned4(n_accepted) || !aligned4(kv_lens_out) ||
       (q_lens && !aligned4(q_lens)) || (page_table && !aligned4(page_table)))
     return ATTN_ERR_INVALID_ARG;
@@ -941,6 +948,11 @@ attn_status_t attn_tree_accept(void* k, void* v, float* k_scale, float* v_scale,
   if (n_q > 64 || B > 65535 || n_layers > 65535) return ATTN_ERR_UNSUPPORTED;
   if (page_table && (long long)max_pages * page_size > 0x7fffffffLL) return ATTN_ERR_UNSUPPORTED;
   if (n_layers == 0) return ATTN_ERR_INVALID_ARG;  // no block would write kv_lens_out
+  // One block of a sequence writes its length while the others still read what it was worked out from.
+  if (overlap4(kv_lens_out, B, kv_lens, B) || overlap4(kv_lens_out, B, q_lens, B) ||
+      overlap4(kv_lens_out, B, n_accepted, B) || overlap4(kv_lens_out, B, path, (long long)B * n_q) ||
+      overlap4(kv_lens_out, B, page_table, (long long)B * max_pages))
+    return ATTN_ERR_INVALID_ARG;
   p.B = B;
   p.n_q = n_q;
   p.max_pages = max_pages;

@@ -283,7 +283,7 @@ ATTN_API attn_status_t attn_decode_tree_paged(const void* q, const void* k_pool,
  * page_table NULL: contiguous caches, num_pages is taken as B and page_size as Tmax; else [B, max_pages].
  * The drafts' slots must lie in pages of one sequence only.  q_lens NULL: n_q everywhere.
  * A sequence with a bad length, count, draft or page keeps its rows and kv_lens_out[b] = kv_lens[b] (site 70).
- * kv_lens_out must not be kv_lens.
+ * kv_lens_out must not overlap kv_lens, q_lens, path, n_accepted or page_table (refused) nor the caches.
  *
  * attn_pages_copy — pages src[i] -> dst[i], i < n, in every layer.  No page may be written twice, nor be
  * both written and read by different pairs (src[i] = dst[i] is allowed and does nothing): such a list,
