@@ -46,6 +46,23 @@ static bool overlap4(const void* a, long long n_a, const void* b, long long n_b)
   return x < y + (uintptr_t)n_b * 4 && y < x + (uintptr_t)n_a * 4;
 }
 
+struct Words {  // an array of n 4-byte elements
+  const void* p;
+  long long n;
+};
+
+// Whether an output shares a byte with an input or with another output.
+template <int IN, int OUT>
+static bool outputs_overlap(const Words (&in)[IN], const Words (&out)[OUT]) {
+  for (int i = 0; i < OUT; ++i) {
+    for (const Words& x : in)
+      if (overlap4(out[i].p, out[i].n, x.p, x.n)) return true;
+    for (int j = 0; j < i; ++j)
+      if (overlap4(out[i].p, out[i].n, out[j].p, out[j].n)) return true;
+  }
+  return false;
+}
+
 // ---------------------------------------------------------------- tensor maps
 
 typedef CUresult (*EncodeTiledFn)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*,
@@ -949,10 +966,10 @@ attn_status_t attn_tree_accept(void* k, void* v, float* k_scale, float* v_scale,
   if (page_table && (long long)max_pages * page_size > 0x7fffffffLL) return ATTN_ERR_UNSUPPORTED;
   if (n_layers == 0) return ATTN_ERR_INVALID_ARG;  // no block would write kv_lens_out
   // One block of a sequence writes its length while the others still read what it was worked out from.
-  if (overlap4(kv_lens_out, B, kv_lens, B) || overlap4(kv_lens_out, B, q_lens, B) ||
-      overlap4(kv_lens_out, B, n_accepted, B) || overlap4(kv_lens_out, B, path, (long long)B * n_q) ||
-      overlap4(kv_lens_out, B, page_table, (long long)B * max_pages))
-    return ATTN_ERR_INVALID_ARG;
+  const Words in[] = {{kv_lens, B}, {q_lens, B}, {n_accepted, B}, {path, (long long)B * n_q},
+                      {page_table, (long long)B * max_pages}};
+  const Words out[] = {{kv_lens_out, B}};
+  if (outputs_overlap(in, out)) return ATTN_ERR_INVALID_ARG;
   p.B = B;
   p.n_q = n_q;
   p.max_pages = max_pages;
@@ -1005,10 +1022,12 @@ attn_status_t attn_pages_compact(void* k, void* v, float* k_scale, float* v_scal
   if (!ref_counts || !refs_out || !page_map || !info || (p.n_entries > 0 && (!page_table || !table_out)))
     return ATTN_ERR_INVALID_ARG;
   if (!aligned4(ref_counts) || !aligned4(refs_out) || !aligned4(page_map) || !aligned4(info) ||
-      !aligned4(page_table) || !aligned4(table_out) || refs_out == ref_counts ||
-      (p.n_entries > 0 && table_out == page_table))
+      !aligned4(page_table) || !aligned4(table_out))
     return ATTN_ERR_INVALID_ARG;
   if (num_pages > kMaxPages) return ATTN_ERR_UNSUPPORTED;
+  const Words in[] = {{page_table, p.n_entries}, {ref_counts, num_pages}};
+  const Words out[] = {{table_out, p.n_entries}, {refs_out, num_pages}, {page_map, num_pages}, {info, 2}};
+  if (outputs_overlap(in, out)) return ATTN_ERR_INVALID_ARG;
   p.table = page_table;
   p.refs = ref_counts;
   p.table_out = table_out;
@@ -1052,12 +1071,16 @@ attn_status_t attn_pages_fork(void* k, void* v, float* k_scale, float* v_scale, 
                         lens_out};
   for (const void* x : ptrs)
     if (!aligned4(x)) return ATTN_ERR_INVALID_ARG;
-  if (ws_bytes < attn_pages_fork_workspace_bytes(n_children, num_pages)) return ATTN_ERR_INVALID_ARG;
-  if (refs_out == ref_counts || (n_children > 0 && (table_out == page_table || lens_out == kv_lens)))
-    return ATTN_ERR_INVALID_ARG;
+  const size_t need = attn_pages_fork_workspace_bytes(n_children, num_pages);
+  if (ws_bytes < need) return ATTN_ERR_INVALID_ARG;
   if ((long long)max_pages * page_size > 0x7fffffffLL || (long long)n_children * max_pages >= (1 << 30) ||
       (long long)B * max_pages > 0x7fffffffLL)
     return ATTN_ERR_UNSUPPORTED;
+  const Words in[] = {{page_table, (long long)B * max_pages}, {kv_lens, B}, {ref_counts, num_pages},
+                      {parents, n_children}, {keep_lens, n_children}, {new_lens, n_children}};
+  const Words out[] = {{table_out, (long long)n_children * max_pages}, {lens_out, n_children}, {refs_out, num_pages},
+                       {info, 2}, {ws, (long long)(need / 4)}};
+  if (outputs_overlap(in, out)) return ATTN_ERR_INVALID_ARG;
   p.B = B;
   p.n_child = n_children;
   p.max_pages = max_pages;

@@ -301,13 +301,14 @@ ATTN_API attn_status_t attn_decode_tree_paged(const void* q, const void* k_pool,
  * new_lens, refs_out [num_pages], info[2] = {free pages left, status}.  If pages are too few, status is
  * ATTN_ERR_BUDGET and info[0] the shortage as a negative number; if a length, parent, table entry or
  * count is bad, status is ATTN_ERR_INVALID_ARG (site 73).  In both cases nothing is copied, refs_out =
- * ref_counts, lens_out = 0, table_out = -1: the old generation stands.  Outputs must not overlap inputs.
+ * ref_counts, lens_out = 0, table_out = -1: the old generation stands.  Outputs (and ws) that overlap inputs or one
+ * another are refused.
  *
  * attn_pages_compact — live pages (ref_counts > 0) at or past n_live, their number, move into the free ones
  * below it, both in rising order.  page_map[p] is where page p went (itself if it stayed, -1 if free);
  * table_out [B, max_pages] and refs_out [num_pages] are the table and counts in the new numbers (entries
  * that are negative, free or outside the pool become -1, the last reported, as are negative counts, with
- * site 72); info[2] = {n_live, pages moved}.  Outputs must not overlap inputs.
+ * site 72); info[2] = {n_live, pages moved}.  Outputs that overlap inputs or one another are refused.
  *
  * Errors: ATTN_ERR_INVALID_ARG for bad sizes, null or misaligned pointers; ATTN_ERR_UNSUPPORTED for n_q > 64,
  * more than 2^20 pages (copy, compact), 2^30 table entries.
