@@ -954,7 +954,7 @@ attn_status_t attn_tree_accept(void* k, void* v, float* k_scale, float* v_scale,
   if (B < 0 || n_q < 0 || n_layers < 0 || (page_table && (max_pages < 1 || page_size < 128 || page_size % 128 != 0)))
     return ATTN_ERR_INVALID_ARG;
   if (B == 0) return ATTN_OK;
-  if (!kv_lens || !path || !n_accepted || !kv_lens_out) return ATTN_ERR_INVALID_ARG;
+  if (!kv_lens || (n_q > 0 && !path) || !n_accepted || !kv_lens_out) return ATTN_ERR_INVALID_ARG;
   if (!aligned4(kv_lens) || !aligned4(path) || !aligned4(n_accepted) || !aligned4(kv_lens_out) ||
       (q_lens && !aligned4(q_lens)) || (page_table && !aligned4(page_table)))
     return ATTN_ERR_INVALID_ARG;
