@@ -659,7 +659,8 @@ def attn_pages_fork(k, v, page_table, kv_lens, ref_counts, parents, *, keep_lens
 def attn_pages_compact(k, v, page_table, ref_counts, *, k_scale=None, v_scale=None, stream=None):
     """Move the live pages (ref_counts > 0) of a pool to its lowest page numbers, in place -> (page_table,
     ref_counts in the new numbers, page_map int32 [num_pages]: where each page went, -1 for free ones,
-    info int32 [2] = live pages, pages moved), all new, parts of one allocation."""
+    info int32 [2] = live pages, pages moved), all new, parts of one allocation.  A negative count moves nothing and
+    gives the old numbers and info -1, 0."""
     device = _one_device(k, v, page_table, ref_counts, k_scale, v_scale)
     layers, pages, page_size, Hkv, row = _cache(k, v, k_scale, v_scale)
     B, max_pages = _table(page_table)

@@ -370,7 +370,22 @@ __global__ void __launch_bounds__(kCopyThreads) pages_compact_kernel(const Compa
     }
     reinterpret_cast<uint32_t*>(bits)[w] = x;
   }
-  __syncthreads();
+  // A count below zero says nothing about who holds the page: whatever moved could land on somebody's.  Every CTA has
+  // read every count, so all of them leave here together, with the old numbers as the new ones.
+  if (__syncthreads_or(negative)) {
+    const long long stride = (long long)gridDim.x * kCopyThreads, first = (long long)blockIdx.x * kCopyThreads + threadIdx.x;
+    for (long long i = first; i < N; i += stride) {
+      p.page_map[i] = (int)i;
+      p.refs_out[i] = p.refs[i];
+    }
+    for (long long i = first; i < p.n_entries; i += stride) p.table_out[i] = p.table[i];
+    if (first == 0) {
+      p.info[0] = -1;
+      p.info[1] = 0;
+      record_arg_error(ATTN_DEV_BAD_INDEX, SITE_PAGES_COMPACT);
+    }
+    return;
+  }
   int total = 0;
   for (int g0 = 0; g0 < groups; g0 += kCopyThreads) {
     const int g = g0 + threadIdx.x;
@@ -413,7 +428,7 @@ __global__ void __launch_bounds__(kCopyThreads) pages_compact_kernel(const Compa
     if (page < n_live) r = L.live(page) ? p.refs[page] : p.refs[L.select(low + page - L.rank(page), false)];
     p.refs_out[page] = r;
   }
-  bool wrong = negative;
+  bool wrong = false;
   for (long long i = first; i < p.n_entries; i += stride) {
     const int t = p.table[i];
     wrong |= t >= N;

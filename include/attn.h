@@ -273,8 +273,8 @@ ATTN_API attn_status_t attn_decode_tree_paged(const void* q, const void* k_pool,
  * neither) hold n_layers layers one behind another: k, v [n_layers, num_pages, page_size, Hkv] rows of
  * row_bytes bytes (D * 2 bf16, D E4M3 or INT8, D / 2 INT4; a multiple of 16), scales [n_layers,
  * num_pages, page_size, Hkv].  All tables, lengths and counts are device int32.  Bad values among them are
- * never used as an index: the call (attn_tree_accept: the sequence) is left undone and
- * attn_device_status reports ATTN_ERR_INVALID_ARG with the site named below.
+ * never used as an index: the call (attn_tree_accept: the sequence; attn_pages_compact: the table entry) is left
+ * undone and attn_device_status reports ATTN_ERR_INVALID_ARG with the site named below.
  *
  * attn_tree_accept — after attn_decode_tree: keep the accepted drafts.  path[b, 0 .. n_accepted[b] - 1]
  * are drafts of sequence b (in [0, q_lens[b])); the cache rows of draft path[b, j], slot base + path[b, j]
@@ -308,8 +308,9 @@ ATTN_API attn_status_t attn_decode_tree_paged(const void* q, const void* k_pool,
  * attn_pages_compact — live pages (ref_counts > 0) at or past n_live, their number, move into the free ones
  * below it, both in rising order.  page_map[p] is where page p went (itself if it stayed, -1 if free);
  * table_out [B, max_pages] and refs_out [num_pages] are the table and counts in the new numbers (entries
- * that are negative, free or outside the pool become -1, the last reported, as are negative counts, with
- * site 72); info[2] = {n_live, pages moved}.  Outputs that overlap inputs or one another are refused.
+ * that are negative, free or outside the pool become -1, the last reported with site 72); info[2] = {n_live, pages
+ * moved}.  A negative count moves nothing (site 72): table_out, refs_out are copies, page_map[p] = p, info = {-1, 0}.
+ * Outputs that overlap inputs or one another are refused.
  *
  * Errors: ATTN_ERR_INVALID_ARG for bad sizes, null or misaligned pointers; ATTN_ERR_UNSUPPORTED for n_q > 64,
  * more than 2^20 pages (copy, compact), 2^30 table entries.
