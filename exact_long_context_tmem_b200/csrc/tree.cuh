@@ -465,8 +465,8 @@ __global__ void __launch_bounds__((TreeCfg<KIND, D, PAIR>::THREADS), 1)
       // A tile is read by the n_rb CTAs of its group at about the same time and never again.
       const uint64_t pol = l2_policy_evict_first();
       const uint32_t q_box = (uint32_t)(p.tps * p.G) * 128u;
-      int u = 0, qi = 0;
-      bool ok = true, q_pending = false;
+      int u = 0, qi = 0;  // units and pieces' queries asked for
+      bool ok = true;
       auto load = [&](const CUtensorMap* tm, const TreePiece& it, int j) -> bool {
         const int tok = (it.t0 + j) * 128;
         const int pg = tree_page(p, it.b, tok), off = tree_page_off(p, tok);
@@ -493,27 +493,29 @@ __global__ void __launch_bounds__((TreeCfg<KIND, D, PAIR>::THREADS), 1)
         if (qi > 0 && !(ok = mbar_wait<true>(q_empty, (qi - 1) & 1, SITE_TR_LOAD))) break;
         uint64_t* q_land = CODED ? q_raw : q_full;
         mbar_arrive_expect_tx(q_land, C::NQ * C::NBOX * q_box);
-        q_pending = true;
         for (int s = 0; s < C::NQ; ++s)
           for (int bx = 0; bx < C::NBOX; ++bx)
             tma_load_5d(smem + C::OFF_Q + s * C::TILE_BYTES + bx * C::BOX_BYTES, &tmQ, q_land, bx * 64, 0,
                         (rb * C::NQ + s) * p.tps, it.kvh, it.b);
+        ++qi;
         if (paired(it)) {
           for (int j = 0; j < it.n && ok; ++j) ok = load(&tmK, it, j) && load(&tmV, it, j);
         } else {
           ok = load(&tmK, it, 0) && (it.n < 2 || load(&tmK, it, 1));
           for (int j = 0; j < it.n && ok; ++j) ok = load(&tmV, it, j) && (j + 2 >= it.n || load(&tmK, it, j + 2));
         }
-        if (!ok) break;
-        ++qi;
-        q_pending = false;
       }
-      if (!ok) {
-        // Let every copy already issued land before the CTA's shared memory is released.
-        if (q_pending) mbar_wait_drain<true>(CODED ? q_raw : q_full, qi & 1, SITE_TR_DRAIN);
-        constexpr int N = CODED ? C::NR : C::NU;
-        uint64_t* full = CODED ? raw_full : u_full;
-        for (int t = (u > N ? u - N : 0); t < u; ++t) mbar_wait_drain<true>(&full[t % N], (t / N) & 1, SITE_TR_DRAIN);
+      // Let every copy asked for land before the CTA's shared memory is released, whatever became of its readers: they
+      // may have given up (another CTA's wait ran out) while this warp had nothing left to wait for.
+      // One loop for the queries (its first turn) and the units: more code here costs the other roles (b4 n64 64K-128K
+      // bf16: 464 us so, 490 with two loops).
+      constexpr int N = CODED ? C::NR : C::NU;
+      const int u0 = max(u - N, 0);
+#pragma unroll 1
+      for (int t = u0 - (qi > 0); t < u; ++t) {
+        const bool is_q = t < u0;
+        uint64_t* bar = is_q ? (CODED ? q_raw : q_full) : (CODED ? raw_full : u_full) + t % N;
+        mbar_wait_drain<true>(bar, (is_q ? qi - 1 : t / N) & 1, SITE_TR_DRAIN);
       }
     }
     __syncwarp();
