@@ -232,7 +232,7 @@ ATTN_API attn_status_t attn_decode_paged(const void* q, const void* k_pool, cons
  * LSE = -inf.  Slots that no row sees are never used, whatever they hold; one that some rows see
  * reaches those rows only (NaN and infinities included).
  *
- *   q, o       device bf16 [B, n_q, Hq, D], n_q <= 64;  lse device float32 [B, n_q, Hq] or NULL
+ *   q, o       device bf16 [B, n_q, Hq, D], n_q <= 64 (o may be q);  lse device float32 [B, n_q, Hq] or NULL
  *   k, v, k_scale, v_scale, page_table, page_size, num_pages, max_pages, kv_lens
  *              as for attn_decode_splitkv / attn_decode_paged, for every cache type; lengths are
  *              clamped to [0, Tmax], a base below 0 leaves slots [0, kv_lens[b]) as the drafts
