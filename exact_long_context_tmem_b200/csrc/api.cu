@@ -605,6 +605,13 @@ static attn_status_t tree_call(const void* q, const void* k, const void* v, attn
 
 // ---------------------------------------------------------------- cache upkeep
 
+// Copy chunks of a page, over all buffers of a layer.
+static long long page_chunks(const CacheBufs& c) {
+  long long n = 0;
+  for (int i = 0; i < c.n; ++i) n += ((long long)c.page_size * c.tok[i] + kChunkBytes - 1) / kChunkBytes;
+  return n;
+}
+
 // The buffers of a cache [layers, pages, page_size, Hkv, row_bytes] with its optional scales, checked.
 static attn_status_t cache_bufs(void* k, void* v, float* ks, float* vs, int n_layers, int num_pages, int page_size,
                                 int Hkv, int row_bytes, CacheBufs* c) {
@@ -618,19 +625,14 @@ static attn_status_t cache_bufs(void* k, void* v, float* ks, float* vs, int n_la
   c->page_size = page_size;
   c->num_pages = num_pages;
   void* ptr[4] = {k, v, ks, vs};
-  long long chunks = 0;
   for (int i = 0; i < c->n; ++i) {
     c->p[i] = static_cast<char*>(ptr[i]);
     c->tok[i] = i < 2 ? Hkv * row_bytes : Hkv * 4;
     c->vec[i] = c->tok[i] % 16 == 0 && aligned16(ptr[i]) ? 16 : 4;
     const long long page = (long long)page_size * c->tok[i];
     c->layer[i] = page * num_pages;
-    c->chunk0[i] = (int)chunks;
-    chunks += (page + kChunkBytes - 1) / kChunkBytes;
-    if (chunks > 0x3fffffff) return ATTN_ERR_UNSUPPORTED;
   }
-  for (int i = c->n; i < 5; ++i) c->chunk0[i] = (int)chunks;
-  return ATTN_OK;
+  return page_chunks(*c) > 0x3fffffff ? ATTN_ERR_UNSUPPORTED : ATTN_OK;
 }
 
 // CTAs for a number of copy chunks: four a processor (see copy_items), fewer when there is less to do.
@@ -1004,7 +1006,7 @@ attn_status_t attn_pages_copy(void* k, void* v, float* k_scale, float* v_scale, 
   const attn_status_t s2 = ensure_smem(pages_copy_kernel, kMaxPages / 8, smem_done);
   if (s2 != ATTN_OK) return s2;
   const int smem = (num_pages + 31) / 32 * 4;
-  pages_copy_kernel<<<copy_grid((long long)n * n_layers * p.c.chunk0[p.c.n]), kCopyThreads, smem,
+  pages_copy_kernel<<<copy_grid((long long)n * n_layers * page_chunks(p.c)), kCopyThreads, smem,
                       reinterpret_cast<cudaStream_t>(stream)>>>(p);
   ATTN_CUDA(cudaGetLastError());
   return ATTN_OK;
@@ -1039,7 +1041,7 @@ attn_status_t attn_pages_compact(void* k, void* v, float* k_scale, float* v_scal
   if (s2 != ATTN_OK) return s2;
   const int smem = (num_pages + 127) / 128 * 20;
   // At most half the pages move.
-  const long long units = std::max<long long>((long long)num_pages / 2 * n_layers * p.c.chunk0[p.c.n],
+  const long long units = std::max<long long>((long long)num_pages / 2 * n_layers * page_chunks(p.c),
                                               std::max<long long>(p.n_entries, num_pages) / kCopyThreads);
   pages_compact_kernel<<<copy_grid(units), kCopyThreads, smem, reinterpret_cast<cudaStream_t>(stream)>>>(p);
   ATTN_CUDA(cudaGetLastError());
@@ -1111,7 +1113,7 @@ attn_status_t attn_pages_fork(void* k, void* v, float* k_scale, float* v_scale, 
   }
   ATTN_CUDA(cudaGetLastError());
   if (n_children == 0) return ATTN_OK;
-  const long long units = std::max<long long>((long long)n_children * n_layers * p.c.chunk0[p.c.n],
+  const long long units = std::max<long long>((long long)n_children * n_layers * page_chunks(p.c),
                                               ((long long)n_children * max_pages + kCopyThreads - 1) / kCopyThreads);
   ATTN_CUDA(launch_dependent(pages_fork_apply_kernel, dim3((unsigned)copy_grid(units)), kCopyThreads, cs, p));
   return ATTN_OK;

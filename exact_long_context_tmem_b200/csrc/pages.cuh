@@ -16,7 +16,6 @@ struct CacheBufs {
   long long layer[4];     // bytes of a layer
   int tok[4];             // bytes of a token
   int vec[4];             // bytes a thread moves at a time: 16, or 4 (scales whose address or size asks for it)
-  int chunk0[5];          // first chunk of each buffer's page, and the chunks of all of them
   int n, n_layers;
   int page_size, num_pages;
 };
@@ -462,7 +461,7 @@ struct ForkParams {
   int* refs_out;
   int* info;     // free pages left (or short of, below zero), status
   // workspace
-  int* child;    // [n_child] pages kept | owner bit 31 ... see ForkChild
+  int* child;    // [n_child] start * 2 + own: its first fresh page in `fresh`, and whether it keeps the page it cuts
   int* copies;   // [n_child][3] source, destination, tokens
   int* fresh;    // [num_pages] free pages in rising order, as many as are taken
   int* count;    // refs after, when they do not fit in shared memory
