@@ -635,9 +635,9 @@ static attn_status_t cache_bufs(void* k, void* v, float* ks, float* vs, int n_la
   return page_chunks(*c) > 0x3fffffff ? ATTN_ERR_UNSUPPORTED : ATTN_OK;
 }
 
-// CTAs for a number of copy chunks: four a processor (see copy_items), fewer when there is less to do.
+// CTAs for a number of copy chunks: kCopyCtas a processor (see copy_items), fewer when there is less to do.
 static int copy_grid(long long units) {
-  return (int)std::max(1LL, std::min<long long>(units, 4LL * sm_count()));
+  return (int)std::max(1LL, std::min<long long>(units, (long long)kCopyCtas * sm_count()));
 }
 
 // ---------------------------------------------------------------- diagnostics

@@ -21,6 +21,8 @@ struct CacheBufs {
 };
 
 static constexpr int kCopyThreads = 256;
+static constexpr int kCopyCtas = 4;  // a processor, which the kernels' registers have to leave room for: at 72 a thread
+                                     // instead of 64 three fit, and a compaction of 4096 pages took 245 us, not 187
 static constexpr int kChunkBytes = kCopyThreads * 2 * 16;  // a CTA has two of them in flight
 static constexpr int kMaxPages = 1 << 20;                  // bitmaps of pages live in shared memory
 
@@ -247,7 +249,7 @@ struct CopyParams {
 
 // Every CTA checks the whole list itself (a bitmap of destinations, n reads from L2), so that all of them
 // refuse a list whose pages are out of range, written twice, or both written and read.
-__global__ void __launch_bounds__(kCopyThreads) pages_copy_kernel(const CopyParams p) {
+__global__ void __launch_bounds__(kCopyThreads, kCopyCtas) pages_copy_kernel(const CopyParams p) {
   extern __shared__ uint32_t written[];
   __shared__ int bad;
   const int words = (p.c.num_pages + 31) / 32;
@@ -339,7 +341,7 @@ struct LivePages {
 
 // Live pages at or past n_live move into the free ones below, both in rising order.  Every CTA builds the
 // bitmap and its prefix itself (4 bytes a page from L2): one launch, and no CTA waits for another.
-__global__ void __launch_bounds__(kCopyThreads) pages_compact_kernel(const CompactParams p) {
+__global__ void __launch_bounds__(kCopyThreads, kCopyCtas) pages_compact_kernel(const CompactParams p) {
   extern __shared__ uint4 bits[];
   __shared__ int warp_sum[kCopyThreads / 32];
   const int N = p.c.num_pages, groups = (N + 127) / 128;
@@ -644,7 +646,7 @@ __global__ void __launch_bounds__(kForkThreads) pages_fork_plan_kernel(const For
 }
 
 // The new table's rows and the kept parts of cut pages, over the whole GPU.
-__global__ void __launch_bounds__(kCopyThreads) pages_fork_apply_kernel(const ForkParams p) {
+__global__ void __launch_bounds__(kCopyThreads, kCopyCtas) pages_fork_apply_kernel(const ForkParams p) {
   grid_dependency_wait();
   const bool fail = p.head[1];
   const int n_copies = p.head[0];
