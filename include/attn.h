@@ -282,7 +282,8 @@ ATTN_API attn_status_t attn_decode_tree_paged(const void* q, const void* k_pool,
  * before any is written (any order and repeats are allowed), and kv_lens_out[b] = base + n_accepted[b].
  * page_table NULL: contiguous caches, num_pages is taken as B and page_size as Tmax; else [B, max_pages].
  * The drafts' slots must lie in pages of one sequence only.  q_lens NULL: n_q everywhere.  n_q = 0 (a step that
- * drafted nothing; path may be NULL) keeps every length.
+ * drafted nothing; path may be NULL) keeps every length.  Pages past a shortened end stay the sequence's: the next
+ * attn_pages_fork takes kv_lens, the lengths that the pages were held for, as before and kv_lens_out as keep_lens.
  * A sequence with a bad length, count, draft or page keeps its rows and kv_lens_out[b] = kv_lens[b] (site 70).
  * kv_lens_out must not overlap kv_lens, q_lens, path, n_accepted or page_table (refused) nor the caches.
  *
@@ -292,7 +293,9 @@ ATTN_API attn_status_t attn_decode_tree_paged(const void* q, const void* k_pool,
  *
  * attn_pages_fork — the next generation of sequences over a pool with shared pages.  Before: B sequences
  * with rows of page_table [B, max_pages], kv_lens[b] tokens in ceil(kv_lens[b] / page_size) pages, and
- * ref_counts[num_pages], the number of table rows that hold each page (plus what the caller pinned).
+ * ref_counts[num_pages], the number of table rows that hold each page (plus what the caller pinned).  kv_lens are the
+ * lengths that the rows hold pages for (the last call's lens_out); with shorter ones the pages past them would stay
+ * counted for good, so what a sequence has lost since is said by keep_lens.
  * After: child c continues parents[c] (-1: nobody) with its first keep = max(0, min(keep_lens[c],
  * kv_lens[parent], new_lens[c])) tokens and has pages for new_lens[c].  So one call forks beams, cuts back
  * rejected drafts, grows, ends (no child) and admits sequences.  Whole kept pages are shared.  A page cut
