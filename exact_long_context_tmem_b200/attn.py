@@ -571,7 +571,8 @@ def attn_tree_accept(k, v, kv_lens, path, n_accepted, *, n_q: int | None = None,
     numbers) names the drafts whose cache rows move, in place and in every layer, to the slots behind
     kv_lens[b] - q_lens[b] (q_lens None: n_q, which defaults to path.shape[1]).  k/v [layers, B, Tmax, Hkv, row] or
     pools [layers, num_pages, page_size, Hkv, row] with page_table [B, max_pages], or one layer without
-    the first dimension -> kv_lens_out int32 [B]."""
+    the first dimension -> kv_lens_out int32 [B].  Pages past a shortened end stay the sequence's until
+    attn_pages_fork, which takes kv_lens as given here and kv_lens_out as keep_lens."""
     device = _one_device(k, v, kv_lens, path, n_accepted, q_lens,
                          page_table, k_scale, v_scale, kv_lens_out)
     layers, pages, page_size, Hkv, row = _cache(k, v, k_scale, v_scale)
@@ -625,8 +626,9 @@ def attn_pages_fork(k, v, page_table, kv_lens, ref_counts, parents, *, keep_lens
     """The next generation of sequences over a pool: child c continues parents[c] (-1: nobody), keeps its
     first keep_lens[c] tokens and has pages for new_lens[c] (all int32 [n_children] on the device).  Whole
     kept pages are shared, cut ones kept or copied, the rest taken from the free pages in rising order; pages
-    nobody holds any more become free.  page_table int32 [B, max_pages], kv_lens int32 [B], ref_counts int32
-    [num_pages] -> (page_table [n_children, max_pages], kv_lens [n_children], ref_counts [num_pages],
+    nobody holds any more become free.  page_table int32 [B, max_pages], kv_lens int32 [B] (the lengths that the
+    rows hold pages for: the last call's, not what attn_tree_accept made of them), ref_counts int32 [num_pages]
+    -> (page_table [n_children, max_pages], kv_lens [n_children], ref_counts [num_pages],
     info int32 [2] = free pages left, status), all new tensors; a status other than 0 (too few pages: budget;
     bad arguments: invalid) leaves the old generation standing.  The new tensors are parts of one allocation."""
     device = _one_device(k, v, page_table, kv_lens, ref_counts, parents,
