@@ -229,8 +229,9 @@ struct TreeCfg {
   static constexpr int THREADS = CODED ? 512 : 384;
   // Register split: the softmax holds a row's 128 scores (bf16) or half of them (coded caches, of whose 512
   // threads a launch has 128 registers each), and the other warpgroups give up what that takes.  The sum
-  // never exceeds what the launch holds (checked on the host before the first launch).  Nothing in a loop may
-  // spill: next to 200 KB of shared memory there is hardly any L1, and a reload takes some 300 cycles.
+  // never exceeds what the launch holds (checked on the host before the first launch).  The coded kernels spill one
+  // 4-byte value (-Xptxas -v: one store, one or five loads), the bf16 ones nothing; more would show: next to 200 KB of
+  // shared memory there is hardly any L1, and a reload takes some 300 cycles.
   static constexpr int REGS_CTRL = CODED ? 96 : 104;  // the MMA issuer of two row slots needs them
   static constexpr int REGS_CONV = 96;
   static constexpr int REGS_SOFTMAX = CODED ? 160 : 200;
@@ -242,9 +243,10 @@ struct TreeCfg {
   static constexpr uint32_t TMEM_COLS = 512;
   // A row's reference may lag its maximum by RESCALE_THRESHOLD and lies REF_DROP below (an upper bound of) it:
   // products reach 2^(4 + 11), of f16's 65504.  A bound may exceed the maximum by REF_SLACK, so the largest
-  // product is at least 2^(11 - 8).  A sum of weights stays below 2^(15 + LOG_MIN's 80) a token.  Measured (b8 n16
-  // t32768 FP8, INT8, INT4 on N(0, 1) values): 203, 218, 214 us with thresholds of 8, drops of 7 and slacks of 8 (floor 2^-24);
-  // 205, 219, 215 as it is (2^-28); 211, 225, 223 with slacks of 7, which send more tiles column by column.
+  // product is at least 2^(11 - 8).  A sum of weights stays below 2^(15 + LOG_MIN's 80) a token.  Measured side by side
+  // (b8 n16 t32768 FP8, INT8, INT4 on N(0, 1) values): 203, 219, 215 us with a threshold of 8, a drop of 7 and a slack of
+  // 8 (floor 2^-24); 205, 219, 215 so (2^-28); 211, 225, 223 with a slack of 7, which sends more tiles column by column.
+  // Where K scales differ so much that every tile goes that way (over 2^4) it takes 246, 259, 251 us, not 198, 214, 206.
   static constexpr float RESCALE_THRESHOLD = CODED ? 4.0f : 8.0f;
   static constexpr float REF_DROP = 11.0f, REF_SLACK = 8.0f;
   static constexpr float LOG_MIN = -80.0f, LOG_MAX = 100.0f;  // of log2 |V scale|
@@ -1095,7 +1097,7 @@ __global__ void __launch_bounds__((TreeCfg<KIND, D, PAIR>::THREADS), 1)
         };
         if constexpr (CODED) {
           // A masked tile has a copy of its own: selects in the common one cost 1500 cycles a tile.  Rows with a power of two
-          // of their own take it too.
+          // of their own take it too (one head in four 2^20 above the others, b8 n16 t32768 FP8: 198 -> 298 us).
           auto weights = [&](auto masked) {
             const float rf = masked.value ? lds_f1(row_at) : 1.f;
             auto scaled = [&](uint32_t a, uint32_t b) -> float2 {
