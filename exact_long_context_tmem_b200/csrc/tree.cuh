@@ -24,17 +24,18 @@
 // that is a whole item is finished here, another leaves a normalised partial in the workspace and
 // tree_join merges an item's partials in tile order (no atomics: results repeat bit for bit).
 //
-// Pipeline, as the prefill's: S = Q K^T in TMEM, one thread per row for the softmax, P (bf16) over S,
-// O += P V; unit ring of MMA-ready K and V tiles in consumption order.  Coded caches (E4M3, INT8, INT4)
+// Pipeline, as the prefill's: S = Q K^T in TMEM, one thread per row for the softmax, P (bf16; f16 for coded
+// caches) over S, O += P V; unit ring of MMA-ready K and V tiles in consumption order.  Coded caches (E4M3, INT8, INT4)
 // land raw in a ring of their own and a fourth warpgroup widens them to f16, which is exact for
 // every code (one instruction per two E4M3 codes, five per four INT8 codes; bf16 took five and eight);
 // the queries follow as f16 times a power of two, one for all of a piece's rows but those far below its largest,
-// which get their own (a padded draft's query may be anything, and is nobody else's business).  The K scale multiplies the fp32 score and the V
-// scale the fp32 weight before its one rounding to f16, so no scale is rounded.  A row's weights are
-// taken relative to its largest weight times V scale, max_t (y_t + log2 |v_scale_t|), not to its largest weight,
-// and from a reference REF_DROP powers of two below it, in f16's upper range: the row's largest product is 2^3 to
-// 2^15, so products down to 2^-17 of it keep f16's full precision whatever the scales and those below are off by
-// at most 2^-28 of it.  (With the largest at 2^-8 to 2^8 a sink token over 128K flat ones cost half of the others' part.)
+// which get their own (a padded draft's query may be anything, and is nobody else's business).  The K scale
+// multiplies the fp32 score and the V scale the fp32 weight before its one rounding to f16, so no scale is
+// rounded.  A row's weights are taken relative to its largest weight times V scale, max_t (y_t + log2
+// |v_scale_t|), not to its largest weight, and from a reference REF_DROP powers of two below it, in f16's upper
+// range: the row's largest product is 2^3 to 2^15, so products down to 2^-17 of it keep f16's full precision
+// whatever the scales and those below are off by at most 2^-28 of it.  (With the largest at 2^-8 to 2^8, 128K flat
+// tokens behind a sink were off by up to half of their part.)
 //
 // Masked places.  Slots past kv_len and drafts no token sees are never used.  A draft that some tokens
 // see may hold anything too: its non-finite V elements enter the MMA as zeros (0 * NaN would reach
@@ -508,9 +509,9 @@ __global__ void __launch_bounds__((TreeCfg<KIND, D, PAIR>::THREADS), 1)
         }
       }
       // Let every copy asked for land before the CTA's shared memory is released, whatever became of its readers: they
-      // may have given up (another CTA's wait ran out) while this warp had nothing left to wait for.
-      // One loop for the queries (its first turn) and the units: more code here costs the other roles (b4 n64 64K-128K
-      // bf16: 464 us so, 490 with two loops).
+      // may have given up (another CTA's wait ran out) while this warp had nothing left to wait for.  One loop for the
+      // queries (its first turn) and the units: more code costs the other roles (b4 n64 64K-128K bf16: 464 us so, 490
+      // with two loops).
       constexpr int N = CODED ? C::NR : C::NU;
       const int u0 = max(u - N, 0);
 #pragma unroll 1

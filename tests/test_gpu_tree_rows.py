@@ -9,6 +9,7 @@ above that, or the scales of the sink's tile alike (the reference then lies 2^10
 
     |o error| <= 2^-8 |o| + (2^-11 + 2^-11) sum_t w_t |v_t|,    |lse error| <= 2^-11 + 2^-20 |lse|.
 """
+import functools
 import math
 
 import numpy as np
@@ -93,6 +94,13 @@ def check_rows(o, lse, ref):
     assert (np.abs(to_np(lse) - rl) <= 2.0**-11 + 2.0**-20 * np.abs(rl)).all()
 
 
+@functools.lru_cache(maxsize=1)  # the three kinds hold the same values
+def sink_case(T, n_q, level, k_ratio, v_shift, where):
+    mask = [(1 << (i + 1)) - 1 for i in range(n_q)]
+    c = sink_cache(T, n_q, 4, level, k_ratio, v_shift, 3, where)
+    return c, mask, rows_in_float64(*c, mask, n_q)
+
+
 @pytest.mark.parametrize("kind", CODED)
 @pytest.mark.parametrize("n_q", [8, 40])
 @pytest.mark.parametrize("T,level,k_ratio,v_shift,where", [(32768, 19, 0.85, 3, 0), (131072, 20, 0.85, 4, 0),
@@ -102,10 +110,9 @@ def check_rows(o, lse, ref):
 def test_a_sink_does_not_cost_the_tail(cuda_device, kind, n_q, T, level, k_ratio, v_shift, where):
     """The tail holds 6 to 35 % of the weight and nearly all of the output; one token far above it, whose scales are the
     smallest of its tile, sets the row's reference."""
-    mask = [(1 << (i + 1)) - 1 for i in range(n_q)]
-    c = sink_cache(T, n_q, 4, level, k_ratio, v_shift, 3, where)
+    c, mask, ref = sink_case(T, n_q, level, k_ratio, v_shift, where)
     o, lse = run_shared(kind, *c, mask, cuda_device)
-    check_rows(o, lse, rows_in_float64(*c, mask, n_q))
+    check_rows(o, lse, ref)
     device_clean()
 
 
