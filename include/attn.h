@@ -281,9 +281,10 @@ ATTN_API attn_status_t attn_decode_tree_paged(const void* q, const void* k_pool,
  * with base = kv_lens[b] - q_lens[b], become slot base + j in every layer, as if all rows were read
  * before any is written (any order and repeats are allowed), and kv_lens_out[b] = base + n_accepted[b].
  * page_table NULL: contiguous caches, num_pages is taken as B and page_size as Tmax; else [B, max_pages].
- * The drafts' slots must lie in pages of one sequence only, each named once in its row.  q_lens NULL: n_q everywhere.  n_q = 0 (a step that
- * drafted nothing; path may be NULL) keeps every length.  Pages past a shortened end stay the sequence's: the next
- * attn_pages_fork takes kv_lens, the lengths that the pages were held for, as before and kv_lens_out as keep_lens.
+ * The drafts' slots must lie in pages of one sequence only, each named once in its row.  q_lens NULL: n_q
+ * everywhere.  n_q = 0 (a step that drafted nothing; path may be NULL) keeps every length.  Pages past a shortened end
+ * stay the sequence's: the next attn_pages_fork takes kv_lens, the lengths that the pages were held for, as before
+ * and kv_lens_out as keep_lens.
  * A sequence with a bad length, count, draft or page keeps its rows and kv_lens_out[b] = kv_lens[b] (site 70).
  * kv_lens_out must not overlap kv_lens, q_lens, path, n_accepted or page_table (refused) nor the caches.
  *
